@@ -190,7 +190,9 @@ CSA_API const char* csa_version(void);
  *   1  a bounded wait (mbarrier / tensor-memory pipeline / cluster
  *      reduction) gave up; the results of that launch are incomplete;
  *   2  the multi-CTA top-k found its score histogram inconsistent with the
- *      scores; that row's top-k output is incomplete (padded with -1).
+ *      scores; that row's top-k output is incomplete (padded with -1);
+ *   4  a paged-cache call met an index out of range or a token without a page
+ *      of its own and left it out (see the paged cache below).
  * Returns CSA_ERR_DEVICE_TIMEOUT if any bit was set. */
 CSA_API csa_status_t csa_device_error(void* workspace, size_t ws_bytes, void* stream, int32_t* code);
 
@@ -474,6 +476,137 @@ CSA_API csa_status_t csa_prefill(const csa_layer_t* L, const csa_cache_t* cache,
                          const int64_t* q_pos, int32_t Tq, int64_t n_max,
                          void* out, int32_t* topk_idx,
                          void* workspace, size_t ws_bytes, void* stream);
+
+/* ============================================================================================
+ * Paged 8-bit key/value cache of grouped-query attention: appending to it, attending over it
+ * (dense, or a sliding window with a few first tokens that stay visible), and the copying, forking,
+ * freeing and compacting of its pages.  For the layers of a stack that are not compressed; the pages
+ * compare the compressed caches against such a grouped-query cache ("DeepSeek-V4: Making a Million
+ * Tokens Affordable") and give none of its details, so the definitions below are this library's.
+ *
+ * Layout.  A page holds `page` consecutive tokens of one sequence: k / v [n_pages][Hkv][page][D] e4m3
+ * codes and one scale per page and KV head, k_scale / v_scale [n_pages][Hkv], a power of two in
+ * [2^-126, 2^120]; value = code * scale.  table[b][p] is the page of tokens [p*page, (p+1)*page) of
+ * sequence b, negative where there is none; refs[g] counts the table entries that name page g (0: free).
+ * Several rows may name one page (after csa_pages_fork); the layers of a stack share one table and
+ * have a pool each.
+ *
+ * Tokens.  A call passes up to Tq new tokens per sequence, j < n_new[b] (all Tq when n_new is NULL),
+ * at positions start[b] + j; n_new[b] is taken into [0, Tq], and a sequence with start[b] < 0 has none.
+ *
+ * Errors on the device.  A page-table entry or page index of n_pages or more, a row index outside [0, B), a position
+ * behind the table, a token without a page of its own, or a reference count that would fall below
+ * zero sets bit 4 of the device error word (the workspace's for csa_paged_attend, the library's own
+ * word for the calls without a workspace, see csa_device_error); the page or token concerned is left
+ * out, nothing is read or written out of range.
+ * ============================================================================================ */
+
+/* One grouped-query attention layer over the cache. */
+typedef struct csa_gqa {
+  int32_t H;             /* query heads, a multiple of Hkv; query head h reads KV head h / (H / Hkv) */
+  int32_t Hkv;           /* KV heads */
+  int32_t D;             /* head dim: 64 or 128 */
+  int32_t act_format;    /* CSA_FMT_F32 | CSA_FMT_BF16: queries, new keys and values, output */
+  int32_t window;        /* keys seen behind the query, itself included; 0: all of them */
+  int32_t first;         /* with a window: the first tokens, which every later query still sees */
+  float softmax_scale;   /* logit scale; 0 selects 1/sqrt(D) */
+  int32_t reserved;      /* 0 */
+} csa_gqa_t;
+
+/* One layer's pages. */
+typedef struct csa_page_pool {
+  void* k;               /* [n_pages][Hkv][page][D] e4m3 codes */
+  void* v;               /* [n_pages][Hkv][page][D] e4m3 codes */
+  float* k_scale;        /* [n_pages][Hkv] */
+  float* v_scale;        /* [n_pages][Hkv] */
+} csa_page_pool_t;
+
+/* The bookkeeping of the pages, shared by the layers. */
+typedef struct csa_page_table {
+  int32_t* table;        /* [B][table_cap]; 4-byte aligned, so that some rows of a table are a table */
+  int32_t* refs;         /* [n_pages] */
+  int64_t table_cap;     /* entries of a row */
+  int64_t n_pages;       /* pages of every pool, at most 2^30 */
+  int32_t B;             /* rows (sequences) */
+  int32_t page;          /* tokens per page: 16, 32, 64 or 128 */
+} csa_page_table_t;
+
+/* Encodes the new tokens' keys and values into their pages.  k_new, v_new: [B][Tq] tokens of Hkv * D
+ * values in act_format, kv_stride elements apart (0: Hkv * D), a multiple of 16 bytes.  Per page and
+ * KV head: scale = the larger of the scale its tokens before start[b] have (nothing when there are
+ * none) and the smallest power of two, at least 2^-126, with max|x| / scale <= 448 over the finite new
+ * values; new codes are x / scale rounded to nearest even, infinities saturated to +-448, NaN kept.
+ * When the scale of a page grows, the codes of its earlier tokens are rounded once more, to the new
+ * scale.  Slots behind the new tokens keep their bytes.  A token is left out, with error bit 4, where
+ * the table has no page for it or refs (unless NULL) says that the page is shared: make the pages
+ * ready with csa_pages_reserve. */
+CSA_API csa_status_t csa_paged_append(const csa_gqa_t* L, const csa_page_pool_t* pool, const csa_page_table_t* T,
+                                      const void* k_new, const void* v_new, int64_t kv_stride,
+                                      const int64_t* start, const int32_t* n_new, int32_t Tq, void* stream);
+
+/* Workspace bytes of csa_paged_attend (host; 0 if an argument is invalid). */
+CSA_API size_t csa_paged_workspace_size(const csa_gqa_t* L, const csa_page_table_t* T, int32_t Tq, int64_t n_max);
+
+/* Attention over the cache.  The query at position t = start[b] + j sees key i of its sequence iff
+ *   i <= t, and (window == 0 or i > t - window or i < first), and table[b][i / page] is a page;
+ *   z_i = <q_h, k_i> * softmax_scale;  o_h = sum_i e^{z_i} v_i / (e^{sinks[h]} + sum_i e^{z_i}),
+ * without the sink's term when sinks is NULL; a query that sees nothing gets 0.  Keys and queries are
+ * taken as they are: rotate them before the call where the layer does.
+ *   q:     [B][Tq] tokens of H * D values in act_format, q_stride elements apart (0: H * D), a multiple
+ *          of 16 bytes; the new tokens' own keys are in the cache already (csa_paged_append)
+ *   sinks: [H] float32 or NULL
+ *   n_max: a bound of every start[b] + n_new[b], at most table_cap * page and 2^30: tokens at n_max or
+ *          behind it are neither attended nor answered
+ *   out:   [B][Tq][H][D] act_format; the rows of tokens j >= n_new[b] are left as they are
+ * Slots that no query sees are not read as numbers: whatever bytes they hold, NaN codes among them,
+ * change nothing.  A NaN among the keys or values that a query sees makes that query's output NaN, at
+ * least in the channels concerned.  Products and sums are float32 or wider; probabilities are rounded to
+ * 11 bits for the product with the values (22 bits when act_format is float32). */
+CSA_API csa_status_t csa_paged_attend(const csa_gqa_t* L, const csa_page_pool_t* pool, const csa_page_table_t* T,
+                                      const void* q, int64_t q_stride, const float* sinks,
+                                      const int64_t* start, const int32_t* n_new, int32_t Tq, int64_t n_max,
+                                      void* out, void* workspace, size_t ws_bytes, void* stream);
+
+/* Row dst[i] of the table becomes a copy of row src[i] (i < n; both int32 on the device), so that the
+ * two share their pages; the pages row dst[i] held before are released.  Pairs are taken from the rows
+ * as they were before the call.  A pair whose src or dst is out of range, whose dst is a src of the
+ * call or the dst of an earlier pair, is left out with error bit 4 (src = dst = -1: left out silently).
+ * n <= 4096. */
+CSA_API csa_status_t csa_pages_fork(const csa_page_table_t* T, const int32_t* src, const int32_t* dst, int32_t n,
+                                    void* stream);
+
+/* Gives every sequence pages of its own for the tokens it is about to write, [start[b], start[b] +
+ * n_new[b]): where the table has none, and where the page there is shared (refs > 1).  When every table
+ * entry that names a shared page is about to write it, the highest row keeps it.  New pages are the
+ * lowest free ones, in the order of rows and positions.  copy_src / copy_dst [B] int32 (output): the
+ * page to copy for row b because it holds tokens before start[b], -1 where there is none; pass them to
+ * csa_pages_copy for every layer before the append.  missing [1] int32 (output): 0, or how many pages
+ * there are too few; then nothing else changes (copy_src, copy_dst all -1).  A sequence whose tokens
+ * pass the end of its row gets nothing, with error bit 4. */
+CSA_API csa_status_t csa_pages_reserve(const csa_page_table_t* T, const int64_t* start, const int32_t* n_new,
+                                       int32_t Tq, int32_t* copy_src, int32_t* copy_dst, int32_t* missing,
+                                       void* stream);
+
+/* Releases pages: entry p of row b is set to -1 and its page's count lowered where
+ *   keep[b] >= 0 and p * page >= keep[b]            (tokens from keep[b] on are dropped; 0 ends the sequence), or
+ *   p * page >= first and (p + 1) * page <= begin[b]  (tokens that a window has left behind for good).
+ * keep, begin: [B] int64 or NULL (at least one given). */
+CSA_API csa_status_t csa_pages_free(const csa_page_table_t* T, const int64_t* keep, const int64_t* begin,
+                                    int64_t first, void* stream);
+
+/* Moves pages down into free ones: the i-th highest page in use goes to the i-th lowest free page, as
+ * long as that is lower and i < max_moves; table and refs are rewritten.  move_src / move_dst
+ * [max_moves] int32 (output, -1 behind the last move) and count [1] int32 (output): pass them to
+ * csa_pages_copy for every layer before the pages are read again.  max_moves <= n_pages. */
+CSA_API csa_status_t csa_pages_compact(const csa_page_table_t* T, int32_t max_moves, int32_t* move_src,
+                                       int32_t* move_dst, int32_t* count, void* stream);
+
+/* Copies page src[i] to page dst[i], codes and scales of keys and values, for i < min(n, count[0])
+ * (count NULL: i < n); src[i] < 0 or dst[i] < 0: nothing.  A page that is named as a dst twice, or as
+ * both a src and a dst, ends with unspecified contents. */
+CSA_API csa_status_t csa_pages_copy(const csa_gqa_t* L, const csa_page_pool_t* pool, const csa_page_table_t* T,
+                                    const int32_t* src, const int32_t* dst, const int32_t* count, int32_t n,
+                                    void* stream);
 
 #ifdef __cplusplus
 }

@@ -55,7 +55,26 @@ class CsaIndexStream(ctypes.Structure):
     _fields_ = [("raw", ctypes.c_void_p), ("gate", ctypes.c_void_p), ("pos_bias", ctypes.c_void_p)]
 
 
+class CsaGqa(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("act_format", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("first", ctypes.c_int32), ("softmax_scale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class CsaPagePool(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class CsaPageTable(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("refs", ctypes.c_void_p), ("table_cap", ctypes.c_int64),
+                ("n_pages", ctypes.c_int64), ("B", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
 _P = ctypes.c_void_p
+_GQA = ctypes.POINTER(CsaGqa)
+_POOL = ctypes.POINTER(CsaPagePool)
+_TABLE = ctypes.POINTER(CsaPageTable)
 _STREAM_S = ctypes.POINTER(CsaIndexStream)
 _LAYER = ctypes.POINTER(CsaLayer)
 _CACHE = ctypes.POINTER(CsaCache)
@@ -94,6 +113,14 @@ _SIGS = {
     "csa_shard_select": (ctypes.c_int, [_LAYER, _I32, _P, _P, _P, _P]),
     "csa_sparse_attend_partial": (ctypes.c_int, [_LAYER, _CACHE, _PARAMS, _P, _P, _P, _I64, _I32, _P, _P, _SZ, _P]),
     "csa_attend_merge": (ctypes.c_int, [_LAYER, _PARAMS, _P, _I32, _P, _P, _P]),
+    "csa_paged_append": (ctypes.c_int, [_GQA, _POOL, _TABLE, _P, _P, _I64, _P, _P, _I32, _P]),
+    "csa_paged_workspace_size": (_SZ, [_GQA, _TABLE, _I32, _I64]),
+    "csa_paged_attend": (ctypes.c_int, [_GQA, _POOL, _TABLE, _P, _I64, _P, _P, _P, _I32, _I64, _P, _P, _SZ, _P]),
+    "csa_pages_fork": (ctypes.c_int, [_TABLE, _P, _P, _I32, _P]),
+    "csa_pages_reserve": (ctypes.c_int, [_TABLE, _P, _P, _I32, _P, _P, _P, _P]),
+    "csa_pages_free": (ctypes.c_int, [_TABLE, _P, _P, _I64, _P]),
+    "csa_pages_compact": (ctypes.c_int, [_TABLE, _I32, _P, _P, _P, _P]),
+    "csa_pages_copy": (ctypes.c_int, [_GQA, _POOL, _TABLE, _P, _P, _P, _I32, _P]),
 }
 
 EXPORTED = tuple(_SIGS)
@@ -163,6 +190,42 @@ def make_index_stream(raw, gate, pos_bias) -> CsaIndexStream:
 def make_params(pos_bias=None, gamma_kv=None, gamma_q=None, sinks=None) -> CsaParams:
     g = lambda t: t.data_ptr() if t is not None else None  # noqa: E731
     return CsaParams(g(pos_bias), g(gamma_kv), g(gamma_q), g(sinks))
+
+
+def make_gqa(H, Hkv, D, window=0, first=0, act_format="bf16", softmax_scale=0.0) -> CsaGqa:
+    return CsaGqa(H, Hkv, D, FMT[act_format], window, first, float(softmax_scale), 0)
+
+
+def _tensor(t, name, dtypes, shape):
+    """Refuses a tensor of another type, shape or layout than the call reads (None in shape: any size)."""
+    if t.dtype not in dtypes:
+        raise CsaError(1, f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.dim() != len(shape) or any(w is not None and w != g for w, g in zip(shape, t.shape)):
+        raise CsaError(1, f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if not t.is_contiguous():
+        raise CsaError(1, f"{name} is not contiguous")
+
+
+def make_page_pool(k, v, k_scale, v_scale) -> CsaPagePool:
+    """Page pool struct over codes [n_pages, Hkv, page, D] (uint8 or float8_e4m3fn) and scales [n_pages, Hkv]
+    (float32).  It keeps the tensors alive."""
+    codes = (torch.uint8, torch.float8_e4m3fn)
+    _tensor(k, "k", codes, (None, None, None, None))
+    _tensor(v, "v", codes, tuple(k.shape))
+    _tensor(k_scale, "k_scale", (torch.float32,), tuple(k.shape[:2]))
+    _tensor(v_scale, "v_scale", (torch.float32,), tuple(k.shape[:2]))
+    p = CsaPagePool(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
+    p.shape, p.keep = tuple(k.shape), (k, v, k_scale, v_scale)
+    return p
+
+
+def make_page_table(table, refs, page) -> CsaPageTable:
+    """Page table struct over table [B, table_cap] and refs [n_pages] (int32).  It keeps the tensors alive."""
+    _tensor(table, "table", (torch.int32,), (None, None))
+    _tensor(refs, "refs", (torch.int32,), (None,))
+    t = CsaPageTable(table.data_ptr(), refs.data_ptr(), table.shape[1], refs.shape[0], table.shape[0], page)
+    t.keep = (table, refs)
+    return t
 
 
 # ----------------------------------------------------------------------------- entry points
@@ -346,3 +409,120 @@ def csa_sparse_attend_partial(L, cache, params, q, q_pos, topk_idx, entry_offset
 def csa_attend_merge(L, params, q_pos, parts, partials, out, stream=None):
     _check(lib().csa_attend_merge(ctypes.byref(L), ctypes.byref(params), ptr(q_pos), parts, ptr(partials), ptr(out),
                                   _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- paged 8-bit cache
+_ACT = {0: torch.float32, 1: torch.bfloat16}
+
+
+def _paged_pool(G, pool, T):
+    """Refuses a pool that is not the layer's or not the table's."""
+    if pool.shape != (T.n_pages, G.Hkv, T.page, G.D):
+        raise CsaError(1, f"pool of {pool.shape}, not {(T.n_pages, G.Hkv, T.page, G.D)} as the layer and the table say")
+
+
+def _ints(t, name, dtype, n):
+    if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous()):
+        raise CsaError(1, f"{name} must be {n} contiguous {dtype}")
+
+
+def _on_device(T, *tensors):
+    """Refuses tensors that are not all on the current device (a kernel there could not read them)."""
+    d = torch.cuda.current_device()
+    for t in (*T.keep, *tensors):
+        if t is not None and (not t.is_cuda or t.get_device() != d):
+            raise CsaError(1, f"a tensor is on {t.device}, not on the current device cuda:{d}")
+
+
+def _token_stride(t, name, G, B, Tq, heads):
+    """Elements between the tokens of t [B, Tq, heads, D] (or [B, Tq, heads * D]), each token contiguous."""
+    if t.dtype != _ACT.get(G.act_format):
+        raise CsaError(1, f"{name} is {t.dtype}, not the layer's activation type")
+    shape, st = tuple(t.shape), t.stride()
+    if shape == (B, Tq, heads, G.D):
+        inner = (st[3] == 1 or G.D == 1) and (st[2] == G.D or heads == 1)
+    elif shape == (B, Tq, heads * G.D):
+        inner = st[2] == 1
+    else:
+        raise CsaError(1, f"{name} has shape {shape}, not {(B, Tq, heads, G.D)}")
+    step = st[1] if Tq > 1 else (st[0] if B > 1 else heads * G.D)
+    if not inner or step < heads * G.D or (B > 1 and st[0] != Tq * step):
+        raise CsaError(1, f"{name}: tokens must be contiguous rows at one distance from each other")
+    return step
+
+
+def csa_paged_append(G, pool, T, k_new, v_new, start, n_new, Tq, stream=None):
+    """k_new, v_new: [B, Tq, Hkv, D]; a view whose tokens lie at one distance (a slice of a fused projection) is
+    taken as it is."""
+    _paged_pool(G, pool, T)
+    stride = _token_stride(k_new, "k_new", G, T.B, Tq, G.Hkv)
+    if _token_stride(v_new, "v_new", G, T.B, Tq, G.Hkv) != stride:
+        raise CsaError(1, "k_new and v_new have tokens at different distances")
+    _ints(start, "start", torch.int64, T.B)
+    _ints(n_new, "n_new", torch.int32, T.B)
+    _on_device(T, *pool.keep, k_new, v_new, start, n_new)
+    _check(lib().csa_paged_append(ctypes.byref(G), ctypes.byref(pool), ctypes.byref(T), ptr(k_new), ptr(v_new), stride,
+                                  ptr(start), ptr(n_new), Tq, _stream(stream)))
+
+
+def csa_paged_workspace_size(G, T, Tq, n_max) -> int:
+    return lib().csa_paged_workspace_size(ctypes.byref(G), ctypes.byref(T), Tq, n_max)
+
+
+def csa_paged_attend(G, pool, T, q, sinks, start, n_new, Tq, n_max, out, workspace, stream=None):
+    """q: [B, Tq, H, D] (tokens at one distance from each other); out: [B, Tq, H, D], contiguous."""
+    _paged_pool(G, pool, T)
+    stride = _token_stride(q, "q", G, T.B, Tq, G.H)
+    if _token_stride(out, "out", G, T.B, Tq, G.H) != G.H * G.D:
+        raise CsaError(1, "out must be contiguous")
+    _ints(start, "start", torch.int64, T.B)
+    _ints(n_new, "n_new", torch.int32, T.B)
+    _ints(sinks, "sinks", torch.float32, G.H)
+    _on_device(T, *pool.keep, q, sinks, start, n_new, out, workspace)
+    _check(lib().csa_paged_attend(ctypes.byref(G), ctypes.byref(pool), ctypes.byref(T), ptr(q), stride, ptr(sinks),
+                                  ptr(start), ptr(n_new), Tq, n_max, ptr(out), ptr(workspace),
+                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def csa_pages_fork(T, src, dst, n, stream=None):
+    _ints(src, "src", torch.int32, n)
+    _ints(dst, "dst", torch.int32, n)
+    _on_device(T, src, dst)
+    _check(lib().csa_pages_fork(ctypes.byref(T), ptr(src), ptr(dst), n, _stream(stream)))
+
+
+def csa_pages_reserve(T, start, n_new, Tq, copy_src, copy_dst, missing, stream=None):
+    _ints(start, "start", torch.int64, T.B)
+    _ints(n_new, "n_new", torch.int32, T.B)
+    _ints(copy_src, "copy_src", torch.int32, T.B)
+    _ints(copy_dst, "copy_dst", torch.int32, T.B)
+    _ints(missing, "missing", torch.int32, 1)
+    _on_device(T, start, n_new, copy_src, copy_dst, missing)
+    _check(lib().csa_pages_reserve(ctypes.byref(T), ptr(start), ptr(n_new), Tq, ptr(copy_src), ptr(copy_dst),
+                                   ptr(missing), _stream(stream)))
+
+
+def csa_pages_free(T, keep, begin, first, stream=None):
+    _ints(keep, "keep", torch.int64, T.B)
+    _ints(begin, "begin", torch.int64, T.B)
+    _on_device(T, keep, begin)
+    _check(lib().csa_pages_free(ctypes.byref(T), ptr(keep), ptr(begin), first, _stream(stream)))
+
+
+def csa_pages_compact(T, max_moves, move_src, move_dst, count, stream=None):
+    _ints(move_src, "move_src", torch.int32, max_moves)
+    _ints(move_dst, "move_dst", torch.int32, max_moves)
+    _ints(count, "count", torch.int32, 1)
+    _on_device(T, move_src, move_dst, count)
+    _check(lib().csa_pages_compact(ctypes.byref(T), max_moves, ptr(move_src), ptr(move_dst), ptr(count),
+                                   _stream(stream)))
+
+
+def csa_pages_copy(G, pool, T, src, dst, count, n, stream=None):
+    _paged_pool(G, pool, T)
+    _ints(src, "src", torch.int32, n)
+    _ints(dst, "dst", torch.int32, n)
+    _ints(count, "count", torch.int32, 1)
+    _on_device(T, *pool.keep, src, dst, count)
+    _check(lib().csa_pages_copy(ctypes.byref(G), ctypes.byref(pool), ctypes.byref(T), ptr(src), ptr(dst), ptr(count), n,
+                                _stream(stream)))

@@ -183,6 +183,7 @@ __device__ __forceinline__ uint32_t float_key(float f) {
 enum : int {
   kErrWaitTimeout = 1,
   kErrTopkOverflow = 2,     // split top-k: appends exceeded their reserved range (inconsistent histogram)
+  kErrPage = 4,             // paged cache: an index out of range, a token without a page of its own
 };
 
 __device__ __forceinline__ void set_device_error(int* err, int bits) {

@@ -1,0 +1,884 @@
+// Attention over the paged 8-bit cache, warp-level tensor-core path (definition: csa_paged_attend in
+// csa.h).  Serves short query blocks (decode, a few speculative tokens) and float32 activations.
+//
+// What bounds it.  A decode step reads 2 D bytes per key and KV head and does 4 D G flops with them
+// (G query heads of the group): at G = 8 that is 16 flops a byte, so memory bounds it.  The design
+// keeps bytes in flight: 8 warps per SM, each with its own ring of 32-key tiles that TMA fills.
+//
+// Work.  A segment is one (sequence, block of query rows, KV head); a row is (token, head of the
+// group).  Its visible keys are cut into tiles of 32 (positions in multiples of 32; with a window, the
+// tiles of the first tokens and then those from the window's start), eight tiles make a unit, and all
+// segments' units in order are dealt to the CTAs in equal runs.  A warp walks every eighth tile of its
+// CTA's run without waiting for the other warps, so copies run ahead over segment borders.  Where a
+// segment ends the CTA merges its warps; a segment cut between CTAs leaves records that a second
+// kernel merges.  Which CTA did what depends on the lengths alone, so results do not change from run
+// to run.
+//
+// Mathematics.  The keys are the M dimension of the products, the query rows the N:
+//   S^T[key][row] = sum_d K[key][d] q[row][d],  O^T[d][row] += sum_key V[key][d] P[key][row]
+// (mma.m16n8k16, f16 inputs, f32 sums), so a group of 8 heads fills the instruction.  e4m3 codes are
+// exact in f16.  Queries are scaled per row by a power of two to at most 2^15 and rounded to f16 (exact
+// for bf16 values down to 2^-32 of the row's largest); float32 queries are the sum of three f16 terms.
+// A lane's 16-byte pieces of K and V need no shuffles: dims are permuted alike in K and q, and V's
+// fragment takes the bytes of two keys by byte permutes.
+// The scale of V's page is folded into the exponent: with z the logit in log2 units and v the log2 of
+// the scale, O sums 2^(z + v - mw), mw the running maximum of z + v, and the denominator sums
+// 2^(z - mz) with its own running maximum mz; both exponentials are cheap here, and neither can lose
+// the other's range however much the pages' scales differ.
+// P is f16 (11 bits): scaled by 2^7, with maxima that move only when a tile exceeds them by more than
+// 8, or (float32) by 2^15 with exact maxima and a second f16 term.  Rounding P is unbiased and f16
+// keeps all 11 bits down to 2^-21 (2^-29) of the largest weight.
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+#include <limits.h>
+#include <mutex>
+
+#include "paged.h"
+#include "sm100.cuh"
+
+namespace csa {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kWarps = 8;
+constexpr int kTile = 32;                     // keys per warp step
+constexpr int kSub = 16;                      // keys per TMA box: within one page
+constexpr float kNone = -3.0e38f;             // a running maximum before any key: finite, below every logit
+
+struct Meta {                                 // one 16-key half of a ring stage
+  float ks, vs;
+};
+
+// One segment's tiles: [0, ta) and [tb, te) in units of 32 positions.
+struct Seg {
+  int b, rb, h;
+  int j0, n;                                  // first token of the block, tokens of the sequence answered
+  int start;
+  int ta, tb, te, tiles, units;
+};
+
+__device__ __forceinline__ int answered(const PagedAttendArgs& a, int b, int* start) {
+  const int64_t s = a.tok.start[b];
+  int n = a.tok.n_new ? a.tok.n_new[b] : a.tok.Tq;
+  n = n < 0 ? 0 : (n > a.tok.Tq ? a.tok.Tq : n);
+  if (s < 0 || s >= a.n_max) n = 0;
+  else if (s + n > a.n_max) n = (int)(a.n_max - s);
+  *start = n ? (int)s : 0;
+  return n;
+}
+
+// Fills the tile range of block rb (`tile` keys to a tile, `per` tiles to a unit).
+__device__ __forceinline__ void seg_range(const PagedAttendArgs& a, Seg& s, int row_tile, int tile, int per) {
+  const int r0 = s.rb * row_tile;
+  s.j0 = r0 / a.G;
+  if (s.j0 >= s.n) {
+    s.ta = s.tb = s.te = s.tiles = s.units = 0;
+    return;
+  }
+  int j1 = (r0 + row_tile - 1) / a.G;
+  j1 = j1 < s.n ? j1 : s.n - 1;
+  const int end = s.start + j1 + 1;
+  int lo = 0, fa = 0;
+  if (a.window > 0) {
+    lo = s.start + s.j0 + 1 - a.window;
+    lo = lo > 0 ? lo : 0;
+    fa = a.first < lo ? a.first : lo;
+  }
+  s.ta = (fa + tile - 1) / tile;
+  s.tb = lo / tile > s.ta ? lo / tile : s.ta;
+  s.te = (end + tile - 1) / tile;
+  if (s.tb > s.te) s.tb = s.te;
+  s.tiles = s.ta + s.te - s.tb;
+  s.units = (s.tiles + per - 1) / per;
+}
+
+__device__ __forceinline__ void seg_load(const PagedAttendArgs& a, Seg& s, int sb, int row_tile, int tile, int per) {
+  s.b = sb / a.rb_max;
+  s.rb = sb - s.b * a.rb_max;
+  s.n = answered(a, s.b, &s.start);
+  seg_range(a, s, row_tile, tile, per);
+}
+
+// This CTA's run of units [u0, u1) of all segments' units; *sb and *before: the (sequence, block) that
+// holds u0 and the units of the segments before it.  All threads of the CTA call it.
+struct Run {
+  int64_t u0, u1, before, total;
+  int sb, ctas;                               // CTAs with work: no more than units
+};
+
+__device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int64_t* scratch) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
+  const int n = a.T.B * a.rb_max;
+  const int each = (n + nt - 1) / nt;
+  int64_t sum = 0;
+  for (int i = tid * each; i < (tid + 1) * each && i < n; ++i) {
+    Seg s;
+    seg_load(a, s, i, row_tile, tile, per);
+    sum += s.units;
+  }
+  sum *= a.Hkv;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) scratch[wid] = inc;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+  for (int w = 0; w < (nt >> 5); ++w) {
+    const int64_t v = scratch[w];
+    if (w < wid) base += v;
+    total += v;
+  }
+  __syncthreads();
+  Run r;
+  r.total = total;
+  r.ctas = total < a.ctas ? (int)total : a.ctas;
+  r.u0 = r.u1 = 0;
+  if ((int)blockIdx.x < r.ctas) {
+    r.u0 = total * blockIdx.x / r.ctas;
+    r.u1 = total * (blockIdx.x + 1) / r.ctas;
+  }
+  int64_t at = base + inc - sum;
+  if (r.u0 < r.u1 && r.u0 >= at && r.u0 < at + sum) {
+    for (int i = tid * each;; ++i) {
+      Seg s;
+      seg_load(a, s, i, row_tile, tile, per);
+      const int64_t u = (int64_t)s.units * a.Hkv;
+      if (r.u0 < at + u) {
+        scratch[0] = i;
+        scratch[1] = at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  r.sb = (int)scratch[0];
+  r.before = scratch[1];
+  __syncthreads();
+  return r;
+}
+
+// Position of a walk over the units of a run.
+struct Walk {
+  Seg s;
+  int sb;
+  int unit;                                   // of the segment
+};
+
+__device__ __forceinline__ void walk_start(const PagedAttendArgs& a, Walk& w, const Run& r, int row_tile, int tile,
+                                           int per) {
+  w.sb = r.sb;
+  seg_load(a, w.s, w.sb, row_tile, tile, per);
+  const int64_t in = r.u0 - r.before;
+  w.s.h = (int)(in / w.s.units);
+  w.unit = (int)(in - (int64_t)w.s.h * w.s.units);
+}
+
+__device__ __forceinline__ void walk_next(const PagedAttendArgs& a, Walk& w, int row_tile, int tile, int per) {
+  if (++w.unit < w.s.units) return;
+  w.unit = 0;
+  if (++w.s.h < a.Hkv) return;
+  w.s.h = 0;
+  const int n = a.T.B * a.rb_max;
+  do {
+    ++w.sb;
+    if (w.sb >= n) return;                    // only behind the last unit
+    seg_load(a, w.s, w.sb, row_tile, tile, per);
+  } while (w.s.units == 0);
+}
+
+__device__ __forceinline__ int tile_pos(const Seg& s, int i, int tile) {
+  return (i < s.ta ? i : s.tb + (i - s.ta)) * tile;
+}
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+      ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Two e4m3 codes (the low 16 bits) as f16 values, exactly; NaN codes become NaN.
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+__device__ __forceinline__ void mma_f16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
+  return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+
+// 2^x: the hardware approximation (relative error about 2^-22, below half of P's rounding) for bf16
+// activations, the correctly scaled function for float32.
+template <bool F32>
+__device__ __forceinline__ float exp2_of(float x) {
+  if (F32) return exp2f(x);
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// NaN codes of four e4m3 bytes as a mask of 0x80 bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+template <int D, int NT, bool F32>
+struct Shape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTerms = F32 ? 3 : 1;
+  static constexpr int kWords = D / 16;                       // k-steps of K q: one 32-bit word of codes per lane
+  static constexpr int kStageBytes = 2 * kTile * D;           // keys, then values
+  static constexpr int kQBytes = kTerms * NT * kWords * 32 * 8;
+  static constexpr int kMergeBytes = 4 * kRows * D * 4;
+  static constexpr int kFixed = kQBytes + kMergeBytes + kRows * 4 + 3 * kWarps * kRows * 4;
+  static constexpr int kFree = 227 * 1024 - 1024 - 512 - kFixed;
+  static constexpr int kFit = kFree / (kWarps * (kStageBytes + 2 * (int)sizeof(Meta) + 8));
+  static constexpr int kStages = kFit < 6 ? kFit : 6;
+  static_assert(kStages >= 2, "ring");
+  // offsets from a 1024-byte boundary
+  static constexpr size_t kOffQ = (size_t)kWarps * kStages * kStageBytes;
+  static constexpr size_t kOffMerge = kOffQ + kQBytes;
+  static constexpr size_t kOffCq = kOffMerge + kMergeBytes;   // [rows] logit factor of a row
+  static constexpr size_t kOffStat = kOffCq + kRows * 4;      // [3][warps][rows]: mw, mz, l
+  static constexpr size_t kOffMeta = kOffStat + 3 * kWarps * kRows * 4;
+  static constexpr size_t kOffBar = (kOffMeta + (size_t)kWarps * kStages * 2 * sizeof(Meta) + 7) / 8 * 8;
+  static constexpr size_t kOffScan = kOffBar + (size_t)kWarps * kStages * 8;
+  static constexpr size_t kBytes = 1024 + kOffScan + kWarps * 8;
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// Floats of one partial record: O [rows][D], then mw, mz, l per row.
+__host__ __device__ constexpr size_t record_floats(int rows, int D) { return (size_t)rows * (D + 3); }
+
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(256, 1)
+paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_constant__ CUtensorMap kmap,
+                    const __grid_constant__ CUtensorMap vmap) {
+  using S = Shape<D, NT, F32>;
+  constexpr int kRows = S::kRows, kTerms = S::kTerms, kWords = S::kWords, kStages = S::kStages;
+  constexpr float kShift = F32 ? 15.f : 7.f;                  // P = 2^(weight + kShift)
+  constexpr float kMargin = F32 ? 0.f : 8.f;
+  extern __shared__ uint8_t raw_smem[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+  uint2* qf = reinterpret_cast<uint2*>(sm + S::kOffQ);        // [terms][NT][words][32 lanes]
+  float* merge = reinterpret_cast<float*>(sm + S::kOffMerge); // [4][rows][D]
+  float* cq = reinterpret_cast<float*>(sm + S::kOffCq);
+  float* stat = reinterpret_cast<float*>(sm + S::kOffStat);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = sm + (size_t)warp * kStages * S::kStageBytes;
+  Meta* meta = reinterpret_cast<Meta*>(sm + S::kOffMeta) + warp * kStages * 2;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::kOffBar) + warp * kStages;
+
+  if (lane == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 3);  // one arrival with the bytes, two of the scales
+    fence_barrier_init();
+  }
+  const Run run = find_run(a, kRows, kTile, kWarps, reinterpret_cast<int64_t*>(sm + S::kOffScan));
+  if (run.u0 >= run.u1) return;
+  const int steps = (int)(run.u1 - run.u0);
+
+  bool ok = true;
+  // ------------------------------------------------------------------ the warp's copies
+  // Lanes 0 and 1 each look after one 16-key half of a tile: its page, its two boxes, its two scales.
+  // The page of the next tile to be copied is loaded one step ahead.
+  Walk pw;                                                    // unit whose tile is copied next
+  walk_start(a, pw, run, kRows, kTile, kWarps);
+  int issued = 0;
+  int32_t page_next = -1;
+  auto load_page = [&]() {
+    page_next = -1;
+    const int i = pw.unit * kWarps + warp;
+    if (lane < 2 && i < pw.s.tiles) {
+      const int pos = tile_pos(pw.s, i, kTile) + kSub * lane;
+      if (pos < pw.s.start + pw.s.n) {                        // at most n_max: inside the table's row
+        const int32_t pg = a.T.table[(size_t)pw.s.b * a.T.cap + (pos >> a.T.page_log2)];
+        if (pg < a.T.n_pages) page_next = pg < 0 ? -1 : pg;
+        else set_device_error(a.err, kErrPage);
+      }
+    }
+  };
+  uint32_t have_bits = 0;                                     // two bits per stage: halves that were copied
+  auto issue = [&]() {
+    const int st = issued % kStages;
+    uint8_t* kd = ring + (size_t)st * S::kStageBytes;
+    const bool mine = lane < 2 && page_next >= 0;
+    const uint32_t have = __ballot_sync(0xffffffffu, mine) & 3u;
+    have_bits = (have_bits & ~(3u << (2 * st))) | (have << (2 * st));
+    if (lane == 0) mbar_arrive_expect_tx(&bars[st], (uint32_t)__popc(have) * (2 * kSub * D));
+    __syncwarp();
+    if (lane < 2) {
+      if (mine) {
+        const int i = pw.unit * kWarps + warp;
+        const int pos = tile_pos(pw.s, i, kTile) + kSub * lane;
+        const int y = pw.s.h * a.T.page + (pos & (a.T.page - 1));
+        tma_load_3d(kd + lane * kSub * D, &kmap, &bars[st], 0, y, page_next);
+        tma_load_3d(kd + kTile * D + lane * kSub * D, &vmap, &bars[st], 0, y, page_next);
+        const size_t gh = (size_t)page_next * a.Hkv + pw.s.h;
+        cp_async4(&meta[2 * st + lane].ks, a.P.ks + gh);
+        cp_async4(&meta[2 * st + lane].vs, a.P.vs + gh);
+      }
+      cp_async_arrive(&bars[st]);
+    }
+    ++issued;
+    if (issued < steps) {
+      walk_next(a, pw, kRows, kTile, kWarps);
+      load_page();
+    }
+  };
+  __syncwarp();
+  load_page();
+  for (int i = 0; i < kStages && i < steps; ++i) issue();
+
+  // ------------------------------------------------------------------ the walk
+  Walk cw;
+  walk_start(a, cw, run, kRows, kTile, kWarps);
+  float o[D / 16][NT][4];
+  float mw[NT][2], mz[NT][2], l[NT][2];
+  int tq[NT][2];                                              // positions of this lane's rows, -1: no such row
+  bool fresh = true;                                          // a segment begins
+  int seg_unit0 = 0;
+  int tmin = 0, tmax = 0;
+  for (int step = 0; step < steps; ++step) {
+    if (fresh) {
+      fresh = false;
+      seg_unit0 = cw.unit;
+      // the block's queries as f16 fragments: warp w takes rows w, w + 8, ...; a lane D / 32 dims
+      __syncthreads();
+      for (int r = warp; r < kRows; r += kWarps) {
+        const int R = cw.s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
+        float x[D / 32];
+        const bool live = j < cw.s.n;
+        if (live) {
+          const size_t at = ((size_t)cw.s.b * a.tok.Tq + j) * a.q_stride + (size_t)(cw.s.h * a.G + gr) * D + lane * (D / 32);
+          if (F32) {
+#pragma unroll
+            for (int u = 0; u < D / 32; ++u) x[u] = reinterpret_cast<const float*>(a.q)[at + u];
+          } else {
+#pragma unroll
+            for (int u = 0; u < D / 32; u += 2) {
+              const uint32_t w = *reinterpret_cast<const uint32_t*>(a.q + 2 * (at + u));
+              x[u] = bf16_bits_to_f(w & 0xFFFFu);
+              x[u + 1] = bf16_bits_to_f(w >> 16);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int u = 0; u < D / 32; ++u) x[u] = 0.f;
+        }
+        float am = 0.f;
+#pragma unroll
+        for (int u = 0; u < D / 32; ++u)
+          if (fabsf(x[u]) < INFINITY) am = fmaxf(am, fabsf(x[u]));
+        am = warp_max(am);
+        int e = 0;
+        if (am > 0.f) frexpf(am, &e);                         // am < 2^e
+        int k = 15 - e;                                       // am 2^k in [2^14, 2^15)
+        k = k > 100 ? 100 : k;
+        if (am == 0.f) k = 0;
+        const float up = ldexpf(1.f, k);
+        if (lane == 0) cq[r] = ldexpf(1.f, -k) * a.scale_log2;
+        // dims lane * D/32 + u: fragment word w = 4 dims, of lane column tt
+        const int d0 = lane * (D / 32);
+#pragma unroll
+        for (int u = 0; u < D / 32; u += 2) {
+          const int d = d0 + u;
+          const int chunk = d >> 4, tt = D == 128 ? chunk >> 1 : chunk;
+          const int w = (D == 128 ? (chunk & 1) * 4 : 0) + ((d >> 2) & 3);
+          float y0 = x[u] * up, y1 = x[u + 1] * up;
+#pragma unroll
+          for (int c = 0; c < kTerms; ++c) {
+            const uint32_t h2 = pack_f16x2(y0, y1);
+            uint32_t* dst = reinterpret_cast<uint32_t*>(&qf[((c * NT + (r >> 3)) * kWords + w) * 32 + (r & 7) * 4 + tt]);
+            dst[(d >> 1) & 1] = h2;
+            const float2 b = unpack_f16x2(h2);
+            y0 -= b.x;
+            y1 -= b.y;
+          }
+        }
+      }
+      __syncthreads();
+      tmin = INT_MAX;
+      tmax = -1;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int R = cw.s.rb * kRows + 8 * n + 2 * t + e, j = R / a.G;
+          tq[n][e] = j < cw.s.n ? cw.s.start + j : -1;
+          mw[n][e] = mz[n][e] = kNone;
+          l[n][e] = 0.f;
+        }
+      tmin = cw.s.start + cw.s.j0;
+      {
+        const int j1 = (cw.s.rb * kRows + kRows - 1) / a.G;
+        tmax = cw.s.start + (j1 < cw.s.n ? j1 : cw.s.n - 1);
+      }
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[m][n][e] = 0.f;
+    }
+    const int st = step % kStages;
+    const uint32_t have = (have_bits >> (2 * st)) & 3u;
+    if (ok && !mbar_wait(&bars[st], (uint32_t)(step / kStages) & 1u)) {
+      ok = false;
+      set_device_error(a.err, kErrWaitTimeout);
+    }
+    const int ti = cw.unit * kWarps + warp;
+    if (have) {
+      const uint8_t* kt = ring + (size_t)st * S::kStageBytes;
+      const uint8_t* vt = kt + kTile * D;
+      const int pos = tile_pos(cw.s, ti, kTile);
+      // every row sees every key of the tile?
+      const bool whole = have == 3u && pos + kTile - 1 <= tmin &&
+                         (a.window == 0 || pos > tmax - a.window || pos + kTile <= a.first);
+      float z[2][NT][4];
+      float lv[2];
+      // S^T, scaled: z = logit (log2 units)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        float acc[F32 ? 2 : 1][NT][4];
+#pragma unroll
+        for (int c = 0; c < (F32 ? 2 : 1); ++c)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[c][n][e] = 0.f;
+        // rows of the boxes are swizzled: 16-byte piece c of row r lies at c ^ (r & 7) (128-byte rows),
+        // c ^ ((r >> 1) & 3) (64-byte rows)
+        const int r0 = s * kSub + g, r1 = r0 + 8;
+        uint4 w0[D / 64], w1[D / 64];
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c) {
+          const int piece = D == 128 ? 2 * t + c : t;
+          const int x0 = D == 128 ? piece ^ (r0 & 7) : piece ^ ((r0 >> 1) & 3);
+          const int x1 = D == 128 ? piece ^ (r1 & 7) : piece ^ ((r1 >> 1) & 3);
+          w0[c] = *reinterpret_cast<const uint4*>(kt + r0 * D + 16 * x0);
+          w1[c] = *reinterpret_cast<const uint4*>(kt + r1 * D + 16 * x1);
+        }
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) {
+          const uint32_t a0 = reinterpret_cast<const uint32_t*>(w0)[w], a1 = reinterpret_cast<const uint32_t*>(w1)[w];
+          const uint32_t fr[4] = {e4m3x2_f16x2(a0), e4m3x2_f16x2(a1), e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(a1 >> 16)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = kTerms - 1; c >= 0; --c) {           // the small terms apart from the large one
+              const uint2 b = qf[((c * NT + n) * kWords + w) * 32 + lane];
+              mma_f16(acc[F32 && c > 0 ? 1 : 0][n], fr, b.x, b.y);
+            }
+          }
+        }
+        const float ks = meta[2 * st + s].ks;
+        lv[s] = (float)((int)((__float_as_uint(meta[2 * st + s].vs) >> 23) & 255u) - 127);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float2 c2 = *reinterpret_cast<const float2*>(&cq[8 * n + 2 * t]);
+          const float f0 = fminf(ks * c2.x, 3.0e38f), f1 = fminf(ks * c2.y, 3.0e38f);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float v = acc[0][n][e];
+            if (F32) v += acc[F32 ? 1 : 0][n][e];
+            z[s][n][e] = v * ((e & 1) ? f1 : f0);
+          }
+        }
+      }
+      // values of this lane's four keys per half: 2t, 2t + 1, 2t + 8, 2t + 9; D / 8 dims
+      constexpr int kVW = D / 32;                             // 32-bit words per key
+      uint32_t vw[2][4][kVW];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int r = s * kSub + 2 * t + (q & 1) + 8 * (q >> 1);
+          if (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vt + r * D + 16 * (g ^ (r & 7)));
+            vw[s][q][0] = x.x; vw[s][q][1] = x.y; vw[s][q][kVW - 2] = x.z; vw[s][q][kVW - 1] = x.w;
+          } else {
+            const uint2 x = *reinterpret_cast<const uint2*>(vt + r * D + 16 * ((g >> 1) ^ ((r >> 1) & 3)) + 8 * (g & 1));
+            vw[s][q][0] = x.x; vw[s][q][1] = x.y;
+          }
+        }
+      if (!whole) {
+        // Some row does not see some key: its value must not enter by 0 * NaN.  NaN codes of V become
+        // 0, and the logit of a key that had one becomes NaN, for the rows that see it.
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          uint32_t bal[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t any = 0;
+#pragma unroll
+            for (int w = 0; w < kVW; ++w) {
+              const uint32_t nb = nan_bytes(vw[s][q][w]);
+              any |= nb;
+              vw[s][q][w] &= ~((nb >> 7) * 0xFFu);
+            }
+            bal[q] = __ballot_sync(0xffffffffu, any != 0);
+          }
+          const uint32_t col = 0x11111111u << (g >> 1);       // lanes that hold key g's values
+          const bool bad0 = ((g & 1) ? bal[1] : bal[0]) & col, bad1 = ((g & 1) ? bal[3] : bal[2]) & col;
+          const bool here = (have >> s) & 1u;
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int i = pos + s * kSub + g + 8 * (e >> 1), tr = tq[n][e & 1];
+              const bool see = here && i <= tr && (a.window == 0 || i > tr - a.window || i < a.first);
+              const bool bad = (e >> 1) ? bad1 : bad0;
+              z[s][n][e] = see ? (bad ? __int_as_float(0x7fffffff) : z[s][n][e]) : -INFINITY;
+            }
+        }
+      }
+      // running maxima
+      bool over = false;
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            over |= z[s][n][e] + lv[s] > mw[n][e & 1] + kMargin || z[s][n][e] > mz[n][e & 1] + 40.f;
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float nz = kNone, nw = kNone;
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              const float h = fmaxf(z[s][n][e], z[s][n][e + 2]);
+              nz = fmaxf(nz, h);
+              nw = fmaxf(nw, h + lv[s]);
+            }
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+              nz = fmaxf(nz, __shfl_xor_sync(0xffffffffu, nz, d));
+              nw = fmaxf(nw, __shfl_xor_sync(0xffffffffu, nw, d));
+            }
+            nz = fmaxf(nz, mz[n][e]);
+            nw = fmaxf(nw, mw[n][e]);
+            l[n][e] *= exp2_of<F32>(mz[n][e] - nz);
+            const float al = exp2_of<F32>(mw[n][e] - nw);
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+              o[m][n][e] *= al;
+              o[m][n][e + 2] *= al;
+            }
+            mz[n][e] = nz;
+            mw[n][e] = nw;
+          }
+      }
+      // P (f16, transposed to [row][key] pairs) and the denominators
+      uint32_t p[2][F32 ? 2 : 1][NT][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[n][e & 1] += exp2_of<F32>(z[s][n][e] - mz[n][e & 1]);
+            y[e] = exp2_of<F32>(z[s][n][e] + (lv[s] - mw[n][e & 1] + kShift));
+          }
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const uint32_t hi = pack_f16x2(y[2 * hf], y[2 * hf + 1]);
+            p[s][0][n][hf] = transpose8x8(hi);
+            if (F32) {
+              const float2 b = unpack_f16x2(hi);
+              p[s][F32 ? 1 : 0][n][hf] = transpose8x8(pack_f16x2(y[2 * hf] - b.x, y[2 * hf + 1] - b.y));
+            }
+          }
+        }
+      // O^T += V^T P^T.  float32: the tile's sums are formed apart and added to O rounded to nearest,
+      // so that the tensor core's truncation does not add up over a long sequence.
+#pragma unroll
+      for (int m = 0; m < D / 16; ++m) {
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[n][e] = F32 ? 0.f : o[m][n][e];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          // dims 2 m and 2 m + 1 of this lane's run: bytes (2 m) & 3 and the next of word m / 2
+          const uint32_t sel = (m & 1) ? 0x7362u : 0x5140u;
+          const uint32_t x = __byte_perm(vw[s][0][m >> 1], vw[s][1][m >> 1], sel);
+          const uint32_t y = __byte_perm(vw[s][2][m >> 1], vw[s][3][m >> 1], sel);
+          const uint32_t fr[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y), e4m3x2_f16x2(y >> 16)};
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (F32) mma_f16(acc[n], fr, p[s][F32 ? 1 : 0][n][0], p[s][F32 ? 1 : 0][n][1]);
+            mma_f16(acc[n], fr, p[s][0][n][0], p[s][0][n][1]);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[m][n][e] = F32 ? o[m][n][e] + acc[n][e] : acc[n][e];
+      }
+    }
+    __syncwarp();                                             // the stage has been read by every lane
+    if (issued < steps && ok) issue();
+
+    // ---------------------------------------------------------------- the segment's end (for this CTA)
+    const bool last_unit = cw.unit + 1 == cw.s.units;
+    if (!last_unit && step + 1 < steps) {
+      ++cw.unit;
+      continue;
+    }
+    // denominators over the lanes that share a row, then the warps' statistics
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], d);
+        if (g == 0) {
+          const int r = 8 * n + 2 * t + e;
+          stat[(0 * kWarps + warp) * kRows + r] = mw[n][e];
+          stat[(1 * kWarps + warp) * kRows + r] = mz[n][e];
+          stat[(2 * kWarps + warp) * kRows + r] = l[n][e];
+        }
+      }
+    __syncthreads();
+    // O relative to the CTA's maximum: warps 4..7 leave theirs, warps 0..3 add their own
+    for (int half = 1; half >= 0; --half) {
+      if ((warp >> 2) == half) {
+        float* mb = merge + (size_t)(warp & 3) * kRows * D;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            float top = kNone;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stat[w * kRows + r]);
+            const float f = exp2f(mw[n][e] - top);
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+              // dims of this lane: g * D/8 + 2 m (+1)
+              float2* at = reinterpret_cast<float2*>(mb + (size_t)r * D + g * (D / 8) + 2 * m);
+              float2 v = make_float2(o[m][n][e] * f, o[m][n][e + 2] * f);
+              if (half == 0) {
+                const float2 b = *at;
+                v.x += b.x;
+                v.y += b.y;
+              }
+              *at = v;
+            }
+          }
+      }
+      __syncthreads();
+    }
+    const bool complete = seg_unit0 == 0 && last_unit;
+    const int seg = cw.sb * a.Hkv + cw.s.h;
+    float* rec = a.part + ((size_t)blockIdx.x * 2 + (seg_unit0 == 0 ? 1 : 0)) * record_floats(kRows, D);
+    for (int i = tid; i < kRows * (D / 4); i += 256) {
+      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+      const int R = cw.s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
+      if (j >= cw.s.n) continue;
+      float W = kNone, Z = kNone, L = 0.f;
+      for (int w = 0; w < kWarps; ++w) {
+        W = fmaxf(W, stat[(0 * kWarps + w) * kRows + r]);
+        Z = fmaxf(Z, stat[(1 * kWarps + w) * kRows + r]);
+      }
+      for (int w = 0; w < kWarps; ++w)
+        L += stat[(2 * kWarps + w) * kRows + r] * exp2f(stat[(1 * kWarps + w) * kRows + r] - Z);
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 b = *reinterpret_cast<const float4*>(merge + ((size_t)q * kRows + r) * D + c);
+        v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
+      }
+      if (complete) {
+        const int head = cw.s.h * a.G + gr;
+        float den = L;
+        if (a.sinks) den += exp2f(a.sinks[head] * kLog2e - Z);
+        // O is relative to W (and 2^kShift), the denominator to Z
+        const float f = Z == kNone && L == 0.f ? 0.f : exp2f(W - Z - kShift) / den;
+        const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+        const size_t at = (((size_t)cw.s.b * a.tok.Tq + j) * a.H + head) * D + c;
+        store_act4(a.out + at * (F32 ? 4 : 2), F32 ? CSA_FMT_F32 : CSA_FMT_BF16, 0, out);
+      } else {
+        *reinterpret_cast<float4*>(rec + (size_t)r * D + c) = v;
+        if (c == 0) {
+          rec[(size_t)kRows * D + r] = W;
+          rec[(size_t)kRows * (D + 1) + r] = Z;
+          rec[(size_t)kRows * (D + 2) + r] = L;
+        }
+      }
+    }
+    if (seg_unit0 == 0 && tid == 0) {
+      // the CTA with the segment's first unit names the CTAs that share it: this one to the one that
+      // has the segment's last unit
+      int2 who = make_int2(0, 0);
+      if (!complete) {
+        const int64_t end = run.u1 + (cw.s.units - 1 - cw.unit);     // one behind the segment's last unit
+        who = make_int2((int)blockIdx.x, (int)((end * run.ctas - 1) / run.total));
+      }
+      a.info[seg] = who;
+    }
+    __syncthreads();                                          // merge and stat are free again
+    if (step + 1 < steps) {
+      walk_next(a, cw, kRows, kTile, kWarps);
+      fresh = true;
+    }
+  }
+  if (!ok) {
+    // give the copies in flight time to land before the CTA's memory is handed on
+    for (int i = 0; i < kStages && i < issued; ++i) mbar_wait(&bars[i], (uint32_t)((issued - 1 - i) / kStages) & 1u);
+  }
+}
+
+// Joins the records of the segments that were cut between CTAs: a block per segment and four rows.
+template <int D, int NT, bool F32>
+__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedAttendArgs a) {
+  constexpr int kRows = 8 * NT;
+  constexpr float kShift = F32 ? 15.f : 7.f;
+  const int seg = blockIdx.x;
+  Seg s;
+  seg_load(a, s, seg / a.Hkv, kRows, kTile, kWarps);
+  s.h = seg % a.Hkv;
+  const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
+  const int R = s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
+  if (s.units == 0 || j >= s.n) return;
+  const int2 who = a.info[seg];
+  if (who.x >= who.y) return;                                 // one CTA had all of it
+  float W = kNone, Z = kNone;
+#pragma unroll 4
+  for (int q = who.x; q <= who.y; ++q) {
+    const float* rec = a.part + ((size_t)q * 2 + (q == who.x ? 1 : 0)) * record_floats(kRows, D) + (size_t)kRows * D + r;
+    W = fmaxf(W, rec[0]);
+    Z = fmaxf(Z, rec[kRows]);
+  }
+  float L = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int q = who.x; q <= who.y; ++q) {
+    const float* rec = a.part + ((size_t)q * 2 + (q == who.x ? 1 : 0)) * record_floats(kRows, D);
+    const float* st = rec + (size_t)kRows * D + r;
+    const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
+    const float f = exp2f(st[0] - W);
+    L += st[2 * kRows] * exp2f(st[kRows] - Z);
+    v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+  }
+  const int head = s.h * a.G + gr;
+  if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
+  const float f = Z == kNone && !(L != L) ? 0.f : exp2f(W - Z - kShift) / L;
+  const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+  const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
+  store_act4(a.out + at * (F32 ? 4 : 2), F32 ? CSA_FMT_F32 : CSA_FMT_BF16, 0, out);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    cudaDriverEntryPointQueryResult q;
+    void* p = nullptr;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// Codes as [n_pages][Hkv * page][D] bytes, read in boxes of `rows` rows of one page and head, swizzled
+// so that equal 16-byte columns of neighbouring rows fall on different banks.
+bool make_pool_map(CUtensorMap* m, const void* base, const PagedAttendArgs& a, int rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t D = (cuuint64_t)a.D, per = (cuuint64_t)a.Hkv * a.T.page;
+  cuuint64_t dims[3] = {D, per, (cuuint64_t)a.T.n_pages};
+  cuuint64_t strides[2] = {D, per * D};
+  cuuint32_t box[3] = {(cuuint32_t)a.D, (cuuint32_t)rows, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, a.D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, int NT, bool F32>
+cudaError_t launch_warp_path(const PagedAttendArgs& a, cudaStream_t s) {
+  CUtensorMap km, vm;
+  if (!make_pool_map(&km, a.P.k, a, kSub) || !make_pool_map(&vm, a.P.v, a, kSub)) return cudaErrorInvalidValue;
+  auto kernel = paged_attend_kernel<D, NT, F32>;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Shape<D, NT, F32>::kBytes);
+  if (e == cudaSuccess)
+    e = launch_kernel(kernel, dim3(a.ctas), dim3(256), Shape<D, NT, F32>::kBytes, s, 0, a, km, vm);
+  if (e == cudaSuccess)
+    e = launch_kernel(paged_combine_kernel<D, NT, F32>, dim3((unsigned)(a.T.B * a.rb_max * a.Hkv), 2 * NT), dim3(D), 0,
+                      s, 0, a);
+  return e;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms) {
+  PagedPlan p;
+  (void)n_max;
+  const int64_t rows = (int64_t)Tq * G;
+  p.path = 1;
+  p.row_tile = rows <= 8 ? 8 : (rows <= 16 || act_fmt == CSA_FMT_F32 ? 16 : 32);
+  p.rb_max = (int)((rows + p.row_tile - 1) / p.row_tile);
+  p.ctas = num_sms;
+  size_t off = 256;                                           // the error word
+  p.info = off;
+  p.info_bytes = (size_t)B * p.rb_max * Hkv * sizeof(int2);
+  off = up256(off + p.info_bytes);
+  p.part = off;
+  p.part_bytes = (size_t)p.ctas * 2 * record_floats(p.row_tile, D) * 4;
+  p.total = up256(off + p.part_bytes);
+  return p;
+}
+
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, cudaStream_t s) {
+  const bool f32 = a.act_fmt == CSA_FMT_F32;
+  if (a.D == 128) {
+    if (f32) return p.row_tile == 8 ? launch_warp_path<128, 1, true>(a, s) : launch_warp_path<128, 2, true>(a, s);
+    return p.row_tile == 8    ? launch_warp_path<128, 1, false>(a, s)
+           : p.row_tile == 16 ? launch_warp_path<128, 2, false>(a, s)
+                              : launch_warp_path<128, 4, false>(a, s);
+  }
+  if (f32) return p.row_tile == 8 ? launch_warp_path<64, 1, true>(a, s) : launch_warp_path<64, 2, true>(a, s);
+  return p.row_tile == 8    ? launch_warp_path<64, 1, false>(a, s)
+         : p.row_tile == 16 ? launch_warp_path<64, 2, false>(a, s)
+                            : launch_warp_path<64, 4, false>(a, s);
+}
+
+}  // namespace csa
