@@ -3,12 +3,12 @@
 //
 // What bounds it.  A decode step reads 2 D bytes per key and KV head and does 4 D G flops with them
 // (G query heads of the group): at G = 8 that is 16 flops a byte, so memory bounds it.  The design
-// keeps bytes in flight: 8 warps per SM, each with its own ring of 32-key tiles that TMA fills.
+// keeps bytes in flight: 8 or 12 warps per SM, each with its own ring of 32-key tiles that TMA fills.
 //
 // Work.  A segment is one (sequence, block of query rows, KV head); a row is (token, head of the
 // group).  Its visible keys are cut into tiles of 32 (positions in multiples of 32; with a window, the
-// tiles of the first tokens and then those from the window's start), eight tiles make a unit, and all
-// segments' units in order are dealt to the CTAs in equal runs.  A warp walks every eighth tile of its
+// tiles of the first tokens and then those from the window's start), as many tiles as warps make a unit, and all
+// segments' units in order are dealt to the CTAs in equal runs.  A warp walks its tile of each unit of its
 // CTA's run without waiting for the other warps, so copies run ahead over segment borders.  Where a
 // segment ends the CTA merges its warps; a segment cut between CTAs leaves records that a second
 // kernel merges.  Which CTA did what depends on the lengths alone, so results do not change from run
@@ -42,7 +42,6 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 8;
 constexpr int kTile = 32;                     // keys per warp step
 constexpr int kSub = 16;                      // keys per TMA box: within one page
 constexpr float kNone = -3.0e38f;             // a running maximum before any key: finite, below every logit
@@ -210,11 +209,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Two e4m3 codes (the low 16 bits) as f16 values, exactly; NaN codes become NaN.
-__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
-  uint32_t r;
-  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(w));
-  return r;
+// Four e4m3 codes as two pairs of f16 values, exactly; NaN codes become NaN.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 __device__ __forceinline__ void mma_f16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
@@ -256,10 +256,15 @@ template <int D, int NT, bool F32>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTerms = F32 ? 3 : 1;
+  // Warps and merge buffers: as many as registers (O takes D/16 x NT x 4 of them) and shared memory allow.
+  static constexpr int kWarps = F32 || NT * D > 256 ? 8 : 12;
+  static constexpr int kBufs = NT * D > 128 ? 2 : 4;
+  static constexpr int kThreads = 32 * kWarps;
+  static constexpr bool kQRegs = NT == 1 && !F32;             // query fragments stay in registers
   static constexpr int kWords = D / 16;                       // k-steps of K q: one 32-bit word of codes per lane
   static constexpr int kStageBytes = 2 * kTile * D;           // keys, then values
   static constexpr int kQBytes = kTerms * NT * kWords * 32 * 8;
-  static constexpr int kMergeBytes = 4 * kRows * D * 4;
+  static constexpr int kMergeBytes = kBufs * kRows * D * 4;
   static constexpr int kFixed = kQBytes + kMergeBytes + kRows * 4 + 3 * kWarps * kRows * 4;
   static constexpr int kFree = 227 * 1024 - 1024 - 512 - kFixed;
   static constexpr int kFit = kFree / (kWarps * (kStageBytes + 2 * (int)sizeof(Meta) + 8));
@@ -281,17 +286,17 @@ struct Shape {
 __host__ __device__ constexpr size_t record_floats(int rows, int D) { return (size_t)rows * (D + 3); }
 
 template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(Shape<D, NT, F32>::kThreads, 1)
 paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_constant__ CUtensorMap kmap,
                     const __grid_constant__ CUtensorMap vmap) {
   using S = Shape<D, NT, F32>;
-  constexpr int kRows = S::kRows, kTerms = S::kTerms, kWords = S::kWords, kStages = S::kStages;
+  constexpr int kRows = S::kRows, kTerms = S::kTerms, kWords = S::kWords, kStages = S::kStages, kWarps = S::kWarps;
   constexpr float kShift = F32 ? 15.f : 7.f;                  // P = 2^(weight + kShift)
   constexpr float kMargin = F32 ? 0.f : 8.f;
   extern __shared__ uint8_t raw_smem[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
   uint2* qf = reinterpret_cast<uint2*>(sm + S::kOffQ);        // [terms][NT][words][32 lanes]
-  float* merge = reinterpret_cast<float*>(sm + S::kOffMerge); // [4][rows][D]
+  float* merge = reinterpret_cast<float*>(sm + S::kOffMerge); // [kBufs][rows][D]
   float* cq = reinterpret_cast<float*>(sm + S::kOffCq);
   float* stat = reinterpret_cast<float*>(sm + S::kOffStat);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
@@ -368,6 +373,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
   bool fresh = true;                                          // a segment begins
   int seg_unit0 = 0;
   int tmin = 0, tmax = 0;
+  uint2 qr[S::kQRegs ? kWords : 1];
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
@@ -427,8 +433,10 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
         }
       }
       __syncthreads();
-      tmin = INT_MAX;
-      tmax = -1;
+      if (S::kQRegs) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w) qr[S::kQRegs ? w : 0] = qf[w * 32 + lane];
+      }
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -491,12 +499,14 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
 #pragma unroll
         for (int w = 0; w < kWords; ++w) {
           const uint32_t a0 = reinterpret_cast<const uint32_t*>(w0)[w], a1 = reinterpret_cast<const uint32_t*>(w1)[w];
-          const uint32_t fr[4] = {e4m3x2_f16x2(a0), e4m3x2_f16x2(a1), e4m3x2_f16x2(a0 >> 16), e4m3x2_f16x2(a1 >> 16)};
+          uint32_t fr[4];
+          e4m3x4_f16(a0, fr[0], fr[2]);
+          e4m3x4_f16(a1, fr[1], fr[3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int c = kTerms - 1; c >= 0; --c) {           // the small terms apart from the large one
-              const uint2 b = qf[((c * NT + n) * kWords + w) * 32 + lane];
+              const uint2 b = S::kQRegs ? qr[S::kQRegs ? w : 0] : qf[((c * NT + n) * kWords + w) * 32 + lane];
               mma_f16(acc[F32 && c > 0 ? 1 : 0][n], fr, b.x, b.y);
             }
           }
@@ -565,12 +575,18 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
       // running maxima
       bool over = false;
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int e = 0; e < 2; ++e) {
+          float top = -INFINITY, topw = -INFINITY;
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            over |= z[s][n][e] + lv[s] > mw[n][e & 1] + kMargin || z[s][n][e] > mz[n][e & 1] + 40.f;
+          for (int s = 0; s < 2; ++s) {
+            const float h = fmaxf(z[s][n][e], z[s][n][e + 2]);
+            top = fmaxf(top, h);
+            topw = fmaxf(topw, h + lv[s]);
+          }
+          over |= topw > mw[n][e] + kMargin || top > mz[n][e] + 40.f;
+        }
       if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -638,7 +654,9 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
           const uint32_t sel = (m & 1) ? 0x7362u : 0x5140u;
           const uint32_t x = __byte_perm(vw[s][0][m >> 1], vw[s][1][m >> 1], sel);
           const uint32_t y = __byte_perm(vw[s][2][m >> 1], vw[s][3][m >> 1], sel);
-          const uint32_t fr[4] = {e4m3x2_f16x2(x), e4m3x2_f16x2(x >> 16), e4m3x2_f16x2(y), e4m3x2_f16x2(y >> 16)};
+          uint32_t fr[4];
+          e4m3x4_f16(x, fr[0], fr[1]);
+          e4m3x4_f16(y, fr[2], fr[3]);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
             if (F32) mma_f16(acc[n], fr, p[s][F32 ? 1 : 0][n][0], p[s][F32 ? 1 : 0][n][1]);
@@ -675,10 +693,11 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
         }
       }
     __syncthreads();
-    // O relative to the CTA's maximum: warps 4..7 leave theirs, warps 0..3 add their own
-    for (int half = 1; half >= 0; --half) {
-      if ((warp >> 2) == half) {
-        float* mb = merge + (size_t)(warp & 3) * kRows * D;
+    // O relative to the CTA's maximum, kBufs warps at a time: the first leave theirs, the others add to it
+#pragma unroll 1
+    for (int turn = 0; turn < kWarps / S::kBufs; ++turn) {
+      if (warp / S::kBufs == turn) {
+        float* mb = merge + (size_t)(warp % S::kBufs) * kRows * D;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -692,7 +711,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
               // dims of this lane: g * D/8 + 2 m (+1)
               float2* at = reinterpret_cast<float2*>(mb + (size_t)r * D + g * (D / 8) + 2 * m);
               float2 v = make_float2(o[m][n][e] * f, o[m][n][e + 2] * f);
-              if (half == 0) {
+              if (turn > 0) {
                 const float2 b = *at;
                 v.x += b.x;
                 v.y += b.y;
@@ -706,7 +725,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
     const bool complete = seg_unit0 == 0 && last_unit;
     const int seg = cw.sb * a.Hkv + cw.s.h;
     float* rec = a.part + ((size_t)blockIdx.x * 2 + (seg_unit0 == 0 ? 1 : 0)) * record_floats(kRows, D);
-    for (int i = tid; i < kRows * (D / 4); i += 256) {
+    for (int i = tid; i < kRows * (D / 4); i += S::kThreads) {
       const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
       const int R = cw.s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
       if (j >= cw.s.n) continue;
@@ -719,7 +738,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
         L += stat[(2 * kWarps + w) * kRows + r] * exp2f(stat[(1 * kWarps + w) * kRows + r] - Z);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < S::kBufs; ++q) {
         const float4 b = *reinterpret_cast<const float4*>(merge + ((size_t)q * kRows + r) * D + c);
         v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
       }
@@ -770,7 +789,7 @@ __global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant_
   constexpr float kShift = F32 ? 15.f : 7.f;
   const int seg = blockIdx.x;
   Seg s;
-  seg_load(a, s, seg / a.Hkv, kRows, kTile, kWarps);
+  seg_load(a, s, seg / a.Hkv, kRows, kTile, Shape<D, NT, F32>::kWarps);
   s.h = seg % a.Hkv;
   const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
   const int R = s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
@@ -838,7 +857,7 @@ cudaError_t launch_warp_path(const PagedAttendArgs& a, cudaStream_t s) {
   auto kernel = paged_attend_kernel<D, NT, F32>;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Shape<D, NT, F32>::kBytes);
   if (e == cudaSuccess)
-    e = launch_kernel(kernel, dim3(a.ctas), dim3(256), Shape<D, NT, F32>::kBytes, s, 0, a, km, vm);
+    e = launch_kernel(kernel, dim3(a.ctas), dim3(Shape<D, NT, F32>::kThreads), Shape<D, NT, F32>::kBytes, s, 0, a, km, vm);
   if (e == cudaSuccess)
     e = launch_kernel(paged_combine_kernel<D, NT, F32>, dim3((unsigned)(a.T.B * a.rb_max * a.Hkv), 2 * NT), dim3(D), 0,
                       s, 0, a);
