@@ -19,8 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libcsa.so")
 TRACE_LIB = os.path.join(HERE, "libcsa_trace.so")
 
-SOURCES = ["compress.cu", "index_score.cu", "topk.cu", "attend.cu", "api.cu", "static_scratch.cu", "debug.cu", "index_decode.cu", "index_prep.cu", "shard.cu", "attend_prefill.cu", "paged_api.cu", "paged.cu", "paged_attend.cu"]
-HEADERS = ["common.cuh", "sm100.cuh", "kernels.h", "paged.h"]
+SOURCES = ["compress.cu", "index_score.cu", "topk.cu", "attend.cu", "api.cu", "static_scratch.cu", "debug.cu", "index_decode.cu", "index_prep.cu", "shard.cu", "attend_prefill.cu", "paged_api.cu", "paged.cu", "paged_attend.cu", "paged_attend_tc.cu"]
+HEADERS = ["common.cuh", "sm100.cuh", "kernels.h", "paged.h", "paged_walk.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

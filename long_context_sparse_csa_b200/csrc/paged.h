@@ -101,12 +101,14 @@ struct PagedAttendArgs {
   float* part;              // [ctas][2] records
 };
 struct PagedPlan {
-  int path;                 // 1: warp-level kernel
+  int path;                 // 1: warp-level kernel, 2: tcgen05 kernel
   int row_tile;             // query rows (token, head of the group) per block
   int rb_max, ctas;
   size_t info, info_bytes, part, part_bytes, total;
 };
 PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms);
+// row_tile: 8 or 16
+cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, cudaStream_t s);
 
 }  // namespace csa

@@ -33,7 +33,7 @@
 #include <limits.h>
 #include <mutex>
 
-#include "paged.h"
+#include "paged_walk.cuh"
 #include "sm100.cuh"
 
 namespace csa {
@@ -44,156 +44,10 @@ using namespace sm100;
 
 constexpr int kTile = 32;                     // keys per warp step
 constexpr int kSub = 16;                      // keys per TMA box: within one page
-constexpr float kNone = -3.0e38f;             // a running maximum before any key: finite, below every logit
 
 struct Meta {                                 // one 16-key half of a ring stage
   float ks, vs;
 };
-
-// One segment's tiles: [0, ta) and [tb, te) in units of 32 positions.
-struct Seg {
-  int b, rb, h;
-  int j0, n;                                  // first token of the block, tokens of the sequence answered
-  int start;
-  int ta, tb, te, tiles, units;
-};
-
-__device__ __forceinline__ int answered(const PagedAttendArgs& a, int b, int* start) {
-  const int64_t s = a.tok.start[b];
-  int n = a.tok.n_new ? a.tok.n_new[b] : a.tok.Tq;
-  n = n < 0 ? 0 : (n > a.tok.Tq ? a.tok.Tq : n);
-  if (s < 0 || s >= a.n_max) n = 0;
-  else if (s + n > a.n_max) n = (int)(a.n_max - s);
-  *start = n ? (int)s : 0;
-  return n;
-}
-
-// Fills the tile range of block rb (`tile` keys to a tile, `per` tiles to a unit).
-__device__ __forceinline__ void seg_range(const PagedAttendArgs& a, Seg& s, int row_tile, int tile, int per) {
-  const int r0 = s.rb * row_tile;
-  s.j0 = r0 / a.G;
-  if (s.j0 >= s.n) {
-    s.ta = s.tb = s.te = s.tiles = s.units = 0;
-    return;
-  }
-  int j1 = (r0 + row_tile - 1) / a.G;
-  j1 = j1 < s.n ? j1 : s.n - 1;
-  const int end = s.start + j1 + 1;
-  int lo = 0, fa = 0;
-  if (a.window > 0) {
-    lo = s.start + s.j0 + 1 - a.window;
-    lo = lo > 0 ? lo : 0;
-    fa = a.first < lo ? a.first : lo;
-  }
-  s.ta = (fa + tile - 1) / tile;
-  s.tb = lo / tile > s.ta ? lo / tile : s.ta;
-  s.te = (end + tile - 1) / tile;
-  if (s.tb > s.te) s.tb = s.te;
-  s.tiles = s.ta + s.te - s.tb;
-  s.units = (s.tiles + per - 1) / per;
-}
-
-__device__ __forceinline__ void seg_load(const PagedAttendArgs& a, Seg& s, int sb, int row_tile, int tile, int per) {
-  s.b = sb / a.rb_max;
-  s.rb = sb - s.b * a.rb_max;
-  s.n = answered(a, s.b, &s.start);
-  seg_range(a, s, row_tile, tile, per);
-}
-
-// This CTA's run of units [u0, u1) of all segments' units; *sb and *before: the (sequence, block) that
-// holds u0 and the units of the segments before it.  All threads of the CTA call it.
-struct Run {
-  int64_t u0, u1, before, total;
-  int sb, ctas;                               // CTAs with work: no more than units
-};
-
-__device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int64_t* scratch) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
-  const int n = a.T.B * a.rb_max;
-  const int each = (n + nt - 1) / nt;
-  int64_t sum = 0;
-  for (int i = tid * each; i < (tid + 1) * each && i < n; ++i) {
-    Seg s;
-    seg_load(a, s, i, row_tile, tile, per);
-    sum += s.units;
-  }
-  sum *= a.Hkv;
-  int64_t inc = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += up;
-  }
-  if (lane == 31) scratch[wid] = inc;
-  __syncthreads();
-  int64_t base = 0, total = 0;
-  for (int w = 0; w < (nt >> 5); ++w) {
-    const int64_t v = scratch[w];
-    if (w < wid) base += v;
-    total += v;
-  }
-  __syncthreads();
-  Run r;
-  r.total = total;
-  r.ctas = total < a.ctas ? (int)total : a.ctas;
-  r.u0 = r.u1 = 0;
-  if ((int)blockIdx.x < r.ctas) {
-    r.u0 = total * blockIdx.x / r.ctas;
-    r.u1 = total * (blockIdx.x + 1) / r.ctas;
-  }
-  int64_t at = base + inc - sum;
-  if (r.u0 < r.u1 && r.u0 >= at && r.u0 < at + sum) {
-    for (int i = tid * each;; ++i) {
-      Seg s;
-      seg_load(a, s, i, row_tile, tile, per);
-      const int64_t u = (int64_t)s.units * a.Hkv;
-      if (r.u0 < at + u) {
-        scratch[0] = i;
-        scratch[1] = at;
-        break;
-      }
-      at += u;
-    }
-  }
-  __syncthreads();
-  r.sb = (int)scratch[0];
-  r.before = scratch[1];
-  __syncthreads();
-  return r;
-}
-
-// Position of a walk over the units of a run.
-struct Walk {
-  Seg s;
-  int sb;
-  int unit;                                   // of the segment
-};
-
-__device__ __forceinline__ void walk_start(const PagedAttendArgs& a, Walk& w, const Run& r, int row_tile, int tile,
-                                           int per) {
-  w.sb = r.sb;
-  seg_load(a, w.s, w.sb, row_tile, tile, per);
-  const int64_t in = r.u0 - r.before;
-  w.s.h = (int)(in / w.s.units);
-  w.unit = (int)(in - (int64_t)w.s.h * w.s.units);
-}
-
-__device__ __forceinline__ void walk_next(const PagedAttendArgs& a, Walk& w, int row_tile, int tile, int per) {
-  if (++w.unit < w.s.units) return;
-  w.unit = 0;
-  if (++w.s.h < a.Hkv) return;
-  w.s.h = 0;
-  const int n = a.T.B * a.rb_max;
-  do {
-    ++w.sb;
-    if (w.sb >= n) return;                    // only behind the last unit
-    seg_load(a, w.s, w.sb, row_tile, tile, per);
-  } while (w.s.units == 0);
-}
-
-__device__ __forceinline__ int tile_pos(const Seg& s, int i, int tile) {
-  return (i < s.ta ? i : s.tb + (i - s.ta)) * tile;
-}
 
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
   asm volatile(
@@ -281,9 +135,6 @@ struct Shape {
   static constexpr size_t kBytes = 1024 + kOffScan + kWarps * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
-
-// Floats of one partial record: O [rows][D], then mw, mz, l per row.
-__host__ __device__ constexpr size_t record_floats(int rows, int D) { return (size_t)rows * (D + 3); }
 
 template <int D, int NT, bool F32>
 __global__ void __launch_bounds__(Shape<D, NT, F32>::kThreads, 1)
@@ -460,7 +311,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
     }
     const int st = step % kStages;
     const uint32_t have = (have_bits >> (2 * st)) & 3u;
-    if (ok && !mbar_wait(&bars[st], (uint32_t)(step / kStages) & 1u)) {
+    if (ok && !__all_sync(0xffffffffu, mbar_wait(&bars[st], (uint32_t)(step / kStages) & 1u))) {
       ok = false;
       set_device_error(a.err, kErrWaitTimeout);
     }
@@ -782,46 +633,6 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
   }
 }
 
-// Joins the records of the segments that were cut between CTAs: a block per segment and four rows.
-template <int D, int NT, bool F32>
-__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedAttendArgs a) {
-  constexpr int kRows = 8 * NT;
-  constexpr float kShift = F32 ? 15.f : 7.f;
-  const int seg = blockIdx.x;
-  Seg s;
-  seg_load(a, s, seg / a.Hkv, kRows, kTile, Shape<D, NT, F32>::kWarps);
-  s.h = seg % a.Hkv;
-  const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
-  const int R = s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
-  if (s.units == 0 || j >= s.n) return;
-  const int2 who = a.info[seg];
-  if (who.x >= who.y) return;                                 // one CTA had all of it
-  float W = kNone, Z = kNone;
-#pragma unroll 4
-  for (int q = who.x; q <= who.y; ++q) {
-    const float* rec = a.part + ((size_t)q * 2 + (q == who.x ? 1 : 0)) * record_floats(kRows, D) + (size_t)kRows * D + r;
-    W = fmaxf(W, rec[0]);
-    Z = fmaxf(Z, rec[kRows]);
-  }
-  float L = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int q = who.x; q <= who.y; ++q) {
-    const float* rec = a.part + ((size_t)q * 2 + (q == who.x ? 1 : 0)) * record_floats(kRows, D);
-    const float* st = rec + (size_t)kRows * D + r;
-    const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
-    const float f = exp2f(st[0] - W);
-    L += st[2 * kRows] * exp2f(st[kRows] - Z);
-    v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
-  }
-  const int head = s.h * a.G + gr;
-  if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
-  const float f = Z == kNone && !(L != L) ? 0.f : exp2f(W - Z - kShift) / L;
-  const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
-  const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
-  store_act4(a.out + at * (F32 ? 4 : 2), F32 ? CSA_FMT_F32 : CSA_FMT_BF16, 0, out);
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -858,46 +669,20 @@ cudaError_t launch_warp_path(const PagedAttendArgs& a, cudaStream_t s) {
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Shape<D, NT, F32>::kBytes);
   if (e == cudaSuccess)
     e = launch_kernel(kernel, dim3(a.ctas), dim3(Shape<D, NT, F32>::kThreads), Shape<D, NT, F32>::kBytes, s, 0, a, km, vm);
-  if (e == cudaSuccess)
-    e = launch_kernel(paged_combine_kernel<D, NT, F32>, dim3((unsigned)(a.T.B * a.rb_max * a.Hkv), 2 * NT), dim3(D), 0,
-                      s, 0, a);
+  if (e == cudaSuccess) e = launch_combine<D>(a, CombineShape{8 * NT, kTile, Shape<D, NT, F32>::kWarps, 1, F32 ? 15.f : 7.f}, s);
   return e;
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
 }  // namespace
 
-PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms) {
-  PagedPlan p;
-  (void)n_max;
-  const int64_t rows = (int64_t)Tq * G;
-  p.path = 1;
-  p.row_tile = rows <= 8 ? 8 : (rows <= 16 || act_fmt == CSA_FMT_F32 ? 16 : 32);
-  p.rb_max = (int)((rows + p.row_tile - 1) / p.row_tile);
-  p.ctas = num_sms;
-  size_t off = 256;                                           // the error word
-  p.info = off;
-  p.info_bytes = (size_t)B * p.rb_max * Hkv * sizeof(int2);
-  off = up256(off + p.info_bytes);
-  p.part = off;
-  p.part_bytes = (size_t)p.ctas * 2 * record_floats(p.row_tile, D) * 4;
-  p.total = up256(off + p.part_bytes);
-  return p;
-}
-
-cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, cudaStream_t s) {
+cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, cudaStream_t s) {
   const bool f32 = a.act_fmt == CSA_FMT_F32;
   if (a.D == 128) {
-    if (f32) return p.row_tile == 8 ? launch_warp_path<128, 1, true>(a, s) : launch_warp_path<128, 2, true>(a, s);
-    return p.row_tile == 8    ? launch_warp_path<128, 1, false>(a, s)
-           : p.row_tile == 16 ? launch_warp_path<128, 2, false>(a, s)
-                              : launch_warp_path<128, 4, false>(a, s);
+    if (f32) return row_tile == 8 ? launch_warp_path<128, 1, true>(a, s) : launch_warp_path<128, 2, true>(a, s);
+    return row_tile == 8 ? launch_warp_path<128, 1, false>(a, s) : launch_warp_path<128, 2, false>(a, s);
   }
-  if (f32) return p.row_tile == 8 ? launch_warp_path<64, 1, true>(a, s) : launch_warp_path<64, 2, true>(a, s);
-  return p.row_tile == 8    ? launch_warp_path<64, 1, false>(a, s)
-         : p.row_tile == 16 ? launch_warp_path<64, 2, false>(a, s)
-                            : launch_warp_path<64, 4, false>(a, s);
+  if (f32) return row_tile == 8 ? launch_warp_path<64, 1, true>(a, s) : launch_warp_path<64, 2, true>(a, s);
+  return row_tile == 8 ? launch_warp_path<64, 1, false>(a, s) : launch_warp_path<64, 2, false>(a, s);
 }
 
 }  // namespace csa

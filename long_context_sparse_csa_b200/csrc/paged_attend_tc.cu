@@ -1,0 +1,804 @@
+// Attention over the paged 8-bit cache on tcgen05 (definition: csa_paged_attend in csa.h): blocks of
+// many query rows (prompt chunks, many speculative tokens), bf16 activations.
+//
+// What bounds it.  With hundreds of rows per KV head the products are 4 D flops per (row, key): the
+// tensor core, and beside it the exponentials (one per 4 D = 512 flops at D = 128: at 16 a clock the
+// same 2,048 clocks per 256 x 128 tile that the products take).  Two groups of 128 rows work in turns:
+// while one group's softmax runs, the tensor core works for the other.
+//
+// Mathematics.  S = q K^T and O += P V with M = 128 query rows, f16 operands (e4m3 codes are exact in
+// f16; queries scaled per row by a power of two), f32 sums in tensor memory; P stays in tensor memory,
+// over S's columns, as the A operand of the second product.  Scales and the two running maxima as in
+// the warp-level kernel: O sums 2^(z + v - mw + 7) codes, z the logit in log2 units and v the log2 of the
+// page's value scale; the denominator sums 2^(z - mz).  One exponential serves both: per 16 keys of a
+// page the weights' sum times 2^(mw - mz - v - 7), unless that factor is beyond 2^80 (pages' scales
+// very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when a
+// tile exceeds it by more than 8 (then O is rescaled in tensor memory), so P stays below 2^15.
+//
+// Roles (640 threads): warp 0 issues the products; warps 4-7 and 8-11 are the two groups' softmax, a
+// thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles: 16-byte loads of codes, one tile ahead in
+// registers, to f16 in the 128-byte swizzle (two stages each).  A job is one (tile, group).  With more
+// than 128 rows (kPair) the groups take different rows of the same tile; otherwise the same rows of
+// alternate tiles, joined by the combine kernel.  Order of the products: QK(j), PV(j - 1); QK of a group
+// overwrites the P that its last PV read, so it waits for that product to complete.
+#include <cuda_fp16.h>
+
+#include "paged_walk.cuh"
+#include "sm100.cuh"
+
+namespace csa {
+
+namespace {
+
+using namespace sm100;
+
+constexpr int kKeys = 128;
+constexpr int kThreads = 640;
+constexpr int kSubs = kKeys / 16;
+constexpr float kShift = 7.f, kMargin = 8.f;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsConvert = 88, kRegsIssue = 48;
+static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
+
+struct __align__(8) TcBars {
+  uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
+  uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], ofree[2];
+  uint64_t recfull, recfree;
+  uint32_t tmem_base;
+};
+
+// A CTA's part of a segment.
+struct Part {
+  Seg s;
+  int sb, unit0, tiles;                       // first tile, number of tiles
+  bool complete;
+};
+
+// Walks the parts of a CTA's run.  (units are single tiles here)
+struct Parts {
+  Walk w;
+  int64_t left;
+};
+
+// A warp's place in its CTA's run, in shared memory: the roles need it rarely and their registers more.
+struct WarpWalk {
+  Parts parts;
+  Part next, cur;
+  int more;
+};
+
+template <int D>
+struct TcShape {
+  static constexpr int kHalf = kKeys * 128;                   // 128 rows of 64 f16 values
+  static constexpr int kTileBytes = kHalf * (D / 64);
+  static constexpr size_t kOffK = 2 * (size_t)kTileBytes;     // after the two groups' queries
+  static constexpr size_t kOffV = 4 * (size_t)kTileBytes;
+  static constexpr size_t kOffCq = 6 * (size_t)kTileBytes;    // [2][128] logit factor of a row
+  static constexpr size_t kOffNan = kOffCq + 2 * 128 * 4;     // [2 stages][32] NaN flags of V's rows, four to a byte
+  static constexpr size_t kOffBars = kOffNan + 64;
+  static constexpr size_t kOffScan = kOffBars + (sizeof(TcBars) + 7) / 8 * 8;
+  static constexpr size_t kOffWalk = kOffScan + (kThreads / 32) * 8;
+  static constexpr size_t kBytes = 1024 + kOffWalk + (kThreads / 32) * sizeof(WarpWalk);
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+__device__ __forceinline__ uint32_t sw128(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
+
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]^T, f16 inputs, fp32 accumulate; A: two f16 values of a row per 32-bit column.
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t* v) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
+
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// A whole warp's wait: true for all its lanes or for none.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ void parts_start(const PagedAttendArgs& a, Parts& p, const Run& run, int row_tile) {
+  walk_start(a, p.w, run, row_tile, kKeys, 1);
+  p.left = run.u1 - run.u0;
+}
+
+__device__ __forceinline__ bool parts_next(const PagedAttendArgs& a, Parts& p, Part& out, int row_tile) {
+  if (p.left <= 0) return false;
+  out.s = p.w.s;
+  out.sb = p.w.sb;
+  out.unit0 = p.w.unit;
+  const int rest = p.w.s.units - p.w.unit;
+  out.tiles = p.left < rest ? (int)p.left : rest;
+  out.complete = p.w.unit == 0 && out.tiles == rest;
+  p.left -= out.tiles;
+  if (p.left > 0) {
+    p.w.unit += out.tiles - 1;
+    walk_next(a, p.w, row_tile, kKeys, 1);
+  }
+  return true;
+}
+
+// Page of the 16 positions from pos on, -1 where there is none (or nothing of the sequence).
+__device__ __forceinline__ int32_t sub_page(const PagedAttendArgs& a, const Seg& s, int pos, bool report) {
+  if (pos >= s.start + s.n) return -1;
+  const int32_t g = a.T.table[(size_t)s.b * a.T.cap + (pos >> a.T.page_log2)];
+  if (g >= a.T.n_pages) {
+    if (report) set_device_error(a.err, kErrPage);
+    return -1;
+  }
+  return g < 0 ? -1 : g;
+}
+
+// First and last position of the block's tokens.
+__device__ __forceinline__ void row_span(const PagedAttendArgs& a, const Seg& s, int row_tile, int* tmin, int* tmax) {
+  const int j1 = (s.rb * row_tile + row_tile - 1) / a.G;
+  *tmin = s.start + s.j0;
+  *tmax = s.start + (j1 < s.n ? j1 : s.n - 1);
+}
+
+__device__ __forceinline__ bool sees_all(const PagedAttendArgs& a, int pos, int tmin, int tmax) {
+  return pos + kKeys - 1 <= tmin && (a.window == 0 || pos > tmax - a.window || pos + kKeys <= a.first);
+}
+
+// Bits c <= x of 32.
+__device__ __forceinline__ uint32_t bits_to(int x) { return x < 0 ? 0u : (x >= 31 ? 0xffffffffu : (2u << x) - 1u); }
+
+// kW: keys that certainly share a page's scales, 16 or 32 (32 from pages of 32 on: half the work per scale).
+template <int D, bool kPair, int kW>
+__global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __grid_constant__ PagedAttendArgs a) {
+  using S = TcShape<D>;
+  constexpr int kRowTile = kPair ? 256 : 128;
+  constexpr int kHalves = D / 64, kScales = kKeys / kW;
+  extern __shared__ uint8_t tc_smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
+  float* cqs = reinterpret_cast<float*>(sm + S::kOffCq);
+  uint8_t* nans = sm + S::kOffNan;
+  TcBars* bars = reinterpret_cast<TcBars*>(sm + S::kOffBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->kfull[i], 128);
+      mbar_init(&bars->kfree[i], 1);
+      mbar_init(&bars->vfull[i], 128);
+      mbar_init(&bars->vfree[i], 1);
+      mbar_init(&bars->qfull[i], 128);
+      mbar_init(&bars->sfull[i], 1);
+      mbar_init(&bars->pfull[i], 128);
+      mbar_init(&bars->pvdone[i], 1);
+      mbar_init(&bars->ofree[i], 128);
+    }
+    mbar_init(&bars->recfull, 128);
+    mbar_init(&bars->recfree, 128);
+    fence_barrier_init();
+  }
+  const Run run = find_run(a, kRowTile, kKeys, 1, reinterpret_cast<int64_t*>(sm + S::kOffScan));
+  if (run.u0 >= run.u1) return;
+  if (warp == 0) {
+    tmem_alloc(&bars->tmem_base, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  WarpWalk& walk = reinterpret_cast<WarpWalk*>(sm + S::kOffWalk)[warp];
+  Part& pt = walk.next;
+  if (lane == 0) parts_start(a, walk.parts, run, kRowTile);
+  auto next_part = [&]() {
+    __syncwarp();
+    if (lane == 0) walk.more = parts_next(a, walk.parts, walk.next, kRowTile);
+    __syncwarp();
+    return walk.more != 0;
+  };
+
+  if (warp < 4) {
+    // ------------------------------------------------------------------ the products
+    regs_dec<kRegsIssue>();
+    if (tid == 0) {
+      const uint32_t idesc_s = instr_desc(128, kKeys, 0u);
+      const uint32_t idesc_o = instr_desc(128, D, 0u) | (1u << 16);          // V: dims-major
+      const uint64_t q_desc = desc_kmajor_sw128(smem_u32(sm));
+      const uint64_t k_desc = desc_kmajor_sw128(smem_u32(sm + S::kOffK));
+      const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(sm + S::kOffV), S::kHalf, 1024u);
+      bool ok = true;
+      uint32_t jobs[2] = {0, 0}, parts_of[2] = {0, 0}, opens[2] = {0, 0};    // of each group, so far
+      uint32_t ktile = 0;                                                    // tiles so far (K and V)
+      // the product P V that is still to be issued
+      bool pend = false;
+      int pg = 0;
+      uint32_t ptile = 0;
+      bool pfirst = false, plast_use = false;
+      uint32_t pjob = 0;
+      auto pv = [&]() {
+        if (!pend) return;
+        pend = false;
+        ok = ok && mbar_wait(&bars->vfull[ptile & 1], (ptile >> 1) & 1u);
+        if (ok && pfirst) {                              // O of the group's last segment has been read
+          ok = mbar_wait(&bars->ofree[pg], (opens[pg] & 1u) ^ 1u);
+          ++opens[pg];
+        }
+        ok = ok && mbar_wait(&bars->pfull[pg], pjob & 1u);
+        if (!ok) return;
+        tc_fence_after();
+        const uint64_t vd = v_desc + (uint64_t)((ptile & 1) * (S::kTileBytes >> 4));
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          umma_f16_ts(tmem + 256u + (uint32_t)(pg * D), tmem + (uint32_t)(pg * 128 + 64 + 8 * kk), vd + (uint64_t)((kk * 2048) >> 4),
+                      idesc_o, (pfirst && kk == 0) ? 0u : 1u);
+        umma_commit(&bars->pvdone[pg]);
+        if (plast_use) umma_commit(&bars->vfree[ptile & 1]);
+      };
+      while (ok && parts_next(a, walk.parts, pt, kRowTile)) {
+        for (int i = 0; i < pt.tiles && ok; ++i, ++ktile) {
+          const uint32_t st = ktile & 1u;
+          ok = mbar_wait(&bars->kfull[st], (ktile >> 1) & 1u);
+          for (int u = 0; u < (kPair ? 2 : 1) && ok; ++u) {
+            const int g = kPair ? u : (i & 1);
+            const bool first = kPair ? i == 0 : i < 2;
+            // the same group twice in a row (a part of an odd number of tiles ended): its P comes first
+            if (pend && pg == g) pv();
+            if (first) {
+              ok = mbar_wait(&bars->qfull[g], parts_of[g] & 1u);
+              ++parts_of[g];
+            }
+            // the group's last P has been read (its columns are S's)
+            if (ok && jobs[g] > 0) ok = mbar_wait(&bars->pvdone[g], (jobs[g] - 1) & 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t qd = q_desc + (uint64_t)(g * (S::kTileBytes >> 4));
+            const uint64_t kd = k_desc + (uint64_t)(st * (S::kTileBytes >> 4));
+#pragma unroll
+            for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                umma_f16(tmem + (uint32_t)(g * 128), qd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk),
+                         kd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk), idesc_s, (h | kk) ? 1u : 0u);
+            umma_commit(&bars->sfull[g]);
+            const bool last_use = !kPair || u == 1;
+            if (last_use) umma_commit(&bars->kfree[st]);
+            pv();
+            pend = true;
+            pg = g;
+            ptile = ktile;
+            pfirst = first;
+            plast_use = last_use;
+            pjob = jobs[g]++;
+          }
+        }
+      }
+      if (ok) pv();
+      if (!ok) set_device_error(a.err, kErrWaitTimeout);
+      // nothing of this thread is in flight when tensor memory is released
+      for (int g = 0; g < 2; ++g)
+        if (jobs[g] > 0) mbar_wait(&bars->pvdone[g], (jobs[g] - 1) & 1u);
+    }
+    __syncwarp();
+  } else if (warp < 12) {
+    // ------------------------------------------------------------------ softmax, a thread a row
+    regs_inc<kRegsSoftmax>();
+    const int g = (warp - 4) >> 2, w4 = warp & 3, row = 32 * w4 + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * w4) << 16);
+    const uint32_t s_addr = lane_addr + (uint32_t)(g * 128), o_addr = lane_addr + 256u + (uint32_t)(g * D);
+    uint8_t* Q = sm + (size_t)g * S::kTileBytes;
+    bool ok = true;
+    uint32_t job = 0, tile0 = 0, shared = 0;            // jobs of this group, tiles of the CTA, segments shared by the groups
+
+    // The group's queries: D / 8 lanes a row, scaled by a power of two to at most 2^15, as f16.
+    auto load_q = [&](const Part& p) {
+      constexpr int kLanes = D / 8, kPer = 32 / kLanes;
+      const int c = lane % kLanes;
+#pragma unroll 4
+      for (int it = 0; it < 32 / kPer; ++it) {
+        const int r = 32 * w4 + it * kPer + lane / kLanes;
+        const int R = p.s.rb * kRowTile + (kPair ? g * 128 : 0) + r, j = R / a.G, gr = R - j * a.G;
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (j < p.s.n)
+          x = *reinterpret_cast<const uint4*>(
+              a.q + 2 * (((size_t)p.s.b * a.tok.Tq + j) * a.q_stride + (size_t)(p.s.h * a.G + gr) * D + 8 * c));
+        const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+        float f[8], am = 0.f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          f[2 * u] = bf16_bits_to_f(xw[u] & 0xFFFFu);
+          f[2 * u + 1] = bf16_bits_to_f(xw[u] >> 16);
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (fabsf(f[u]) < INFINITY) am = fmaxf(am, fabsf(f[u]));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) am = fmaxf(am, __shfl_xor_sync(0xffffffffu, am, o));
+        // am < 2^e, e from the exponent field (a subnormal maximum counts as 2^-126)
+        int k = 15 - ((int)(__float_as_uint(am) >> 23) - 126);
+        k = am == 0.f ? 0 : (k > 100 ? 100 : k);
+        const float up = __uint_as_float((uint32_t)(k + 127) << 23);
+        if (c == 0) cqs[g * 128 + r] = __uint_as_float((uint32_t)(127 - k) << 23) * a.scale_log2;
+        uint4 y;
+        y.x = pack_f16x2(f[0] * up, f[1] * up);
+        y.y = pack_f16x2(f[2] * up, f[3] * up);
+        y.z = pack_f16x2(f[4] * up, f[5] * up);
+        y.w = pack_f16x2(f[6] * up, f[7] * up);
+        *reinterpret_cast<uint4*>(Q + (c >> 3) * S::kHalf + sw128(r, c & 7)) = y;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();                                      // cqs: a warp's rows are its own
+      mbar_arrive(&bars->qfull[g]);
+    };
+
+    bool more = next_part();
+    if (more && (kPair || pt.tiles > g)) load_q(pt);
+    while (more && ok) {
+      __syncwarp();
+      if (lane == 0) walk.cur = walk.next;
+      __syncwarp();
+      const Part& cur = walk.cur;
+      const int jobs = kPair ? cur.tiles : (cur.tiles - g + 1) / 2;
+      float mw = kNone, mz = kNone, l = 0.f;
+      const int R = cur.s.rb * kRowTile + (kPair ? g * 128 : 0) + row, j = R / a.G, gr = R - j * a.G;
+      const int t = j < cur.s.n ? cur.s.start + j : -1;
+      int tmin, tmax;
+      row_span(a, cur.s, kRowTile, &tmin, &tmax);
+      const float cq = cqs[g * 128 + row];
+      // lane u < 8: page and scales of the tile's u-th 16 keys, one job ahead
+      auto tile_of = [&](int i) { return kPair ? i : 2 * i + g; };
+      auto scales = [&](int i, float& ks, float& lv) {
+        ks = 0.f;
+        lv = 0.f;
+        bool there = false;
+        if (i < jobs && lane < kSubs) {
+          const int pos = tile_pos(cur.s, cur.unit0 + tile_of(i), kKeys) + 16 * lane;
+          const int32_t pg = sub_page(a, cur.s, pos, false);
+          if (pg >= 0) {
+            const size_t gh = (size_t)pg * a.Hkv + cur.s.h;
+            there = true;
+            ks = a.P.ks[gh];
+            lv = (float)((int)((__float_as_uint(a.P.vs[gh]) >> 23) & 255u) - 127);
+          }
+        }
+        return __ballot_sync(0xffffffffu, there) & 0xFFu;
+      };
+      float nks, nlv;
+      uint32_t nhave = scales(0, nks, nlv);
+      for (int i = 0; i < jobs && ok; ++i, ++job) {
+        const float ks = nks, lvs = nlv;
+        const uint32_t have = nhave;
+        nhave = scales(i + 1, nks, nlv);
+        const int ti = tile_of(i);
+        const int pos = tile_pos(cur.s, cur.unit0 + ti, kKeys);
+        const bool whole = have == 0xFFu && sees_all(a, pos, tmin, tmax);
+        const uint32_t tile = tile0 + (uint32_t)ti;
+        if (!warp_wait(&bars->sfull[g], job & 1u)) { ok = false; break; }
+        if (!whole && !warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u)) { ok = false; break; }   // the NaN flags
+        tc_fence_after();
+        // Half of the tile's scores (64 columns) in registers at a time: the maxima of the first half, then of
+        // the second; P of the second while it is there; the first half read once more.  P takes columns
+        // [64, 128) of S, so that what is written has always been read.
+        float x[64];
+        auto fetch = [&](int hb) {
+          __syncwarp();
+          tmem_ld_32x32b_x32(s_addr + 64u * hb, x);
+          tmem_ld_32x32b_x32(s_addr + 64u * hb + 32u, x + 32);
+          tmem_wait_ld();
+        };
+        auto hide = [&](int hb) {                        // masked scores to -inf, NaN where V's row has one
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int q = 2 * hb + k, p0 = pos + 32 * q;
+            uint32_t m = bits_to(t - p0);
+            if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
+            const uint32_t hv = (have >> (2 * q)) & 3u;
+            m &= ((hv & 1u) ? 0xFFFFu : 0u) | ((hv & 2u) ? 0xFFFF0000u : 0u);
+            if (t < 0) m = 0u;
+            const uint2 nb = *reinterpret_cast<const uint2*>(nans + (tile & 1) * 32 + 8 * q);
+            if (nb.x | nb.y) {
+              uint32_t nan32 = 0;
+#pragma unroll
+              for (int c = 0; c < 4; ++c)
+                nan32 |= ((nb.x >> (8 * c)) & 15u) << (4 * c) | ((nb.y >> (8 * c)) & 15u) << (16 + 4 * c);
+#pragma unroll
+              for (int c = 0; c < 32; ++c)
+                if ((nan32 >> c) & 1u) x[32 * k + c] = __int_as_float(0x7fffffff);
+            }
+#pragma unroll
+            for (int c = 0; c < 32; ++c) x[32 * k + c] = (m >> c) & 1u ? x[32 * k + c] : -INFINITY;
+          }
+        };
+        float fs[kScales], ls[kScales];                  // logit factor and log2 of the value scale per kW columns
+#pragma unroll
+        for (int u = 0; u < kScales; ++u) {
+          fs[u] = fmaxf(fminf(__shfl_sync(0xffffffffu, ks, u * (kW / 16)) * cq, 3.0e38f), 1.2e-38f);
+          ls[u] = __shfl_sync(0xffffffffu, lvs, u * (kW / 16));
+        }
+        float cz = -INFINITY, cw = -INFINITY;
+        auto maxima = [&](int hb) {
+#pragma unroll
+          for (int v = 0; v < 64 / kW; ++v) {
+            const int u = hb * (64 / kW) + v;
+            float t0 = fmaxf(x[kW * v], x[kW * v + 1]), t1 = fmaxf(x[kW * v + 2], x[kW * v + 3]);
+#pragma unroll
+            for (int c = 4; c < kW; c += 4) {
+              t0 = fmaxf(t0, fmaxf(x[kW * v + c], x[kW * v + c + 1]));
+              t1 = fmaxf(t1, fmaxf(x[kW * v + c + 2], x[kW * v + c + 3]));
+            }
+            const float zt = fmaxf(t0, t1) * fs[u];
+            cz = fmaxf(cz, zt);
+            cw = fmaxf(cw, zt + ls[u]);
+          }
+        };
+        fetch(0);
+        if (!whole) hide(0);
+        maxima(0);
+        fetch(1);
+        if (!whole) hide(1);
+        maxima(1);
+        const bool move = cw > mw + kMargin || cz > mz + 40.f;
+        if (__any_sync(0xffffffffu, move)) {
+          const float nw = move ? fmaxf(mw, cw) : mw, nz = move ? fmaxf(mz, cz) : mz;
+          const float al = ex2(mw - nw);
+          l *= ex2(mz - nz);
+          mw = nw;
+          mz = nz;
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
+              tmem_wait_ld();
+              uint32_t ow[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
+              tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
+            }
+          }
+        }
+        auto weigh = [&](int hb) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t p[16];
+#pragma unroll
+            for (int v = 0; v < 32 / kW; ++v) {
+              const int u = (2 * hb + k) * (32 / kW) + v;
+              const float* xs = x + 32 * k + kW * v;
+              const float b = ls[u] - mw + kShift;
+              const float back = mw - mz - ls[u] - kShift;
+              if (back > 80.f) {
+                float apart = 0.f;
+#pragma unroll
+                for (int c = 0; c < kW; ++c) apart += ex2(xs[c] * fs[u] - mz);
+                l += apart;
+              }
+              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+              const float2 f2 = make_float2(fs[u], fs[u]), b2 = make_float2(b, b);
+#pragma unroll
+              for (int c = 0; c < kW; c += 4) {
+                float2 y0 = fma2(make_float2(xs[c], xs[c + 1]), f2, b2);
+                float2 y1 = fma2(make_float2(xs[c + 2], xs[c + 3]), f2, b2);
+                y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+                s0 = add2(s0, y0);
+                s1 = add2(s1, y1);
+                p[(kW * v + c) / 2] = pack_f16x2(y0.x, y0.y);
+                p[(kW * v + c) / 2 + 1] = pack_f16x2(y1.x, y1.y);
+              }
+              s0 = add2(s0, s1);
+              if (!(back > 80.f)) l = fmaf(s0.x + s0.y, ex2(back), l);
+            }
+            __syncwarp();                                // rows may have parted above
+            tmem_st_32x32b_x16(s_addr + 64u + 32u * hb + 16u * k, p);
+          }
+        };
+        weigh(1);
+        fetch(0);
+        if (!whole) hide(0);
+        weigh(0);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(&bars->pfull[g]);
+      }
+      tile0 += (uint32_t)cur.tiles;
+      // the next part's queries, while the last product runs
+      more = next_part();
+      if (ok && more && (kPair || pt.tiles > g)) load_q(pt);
+      if (!ok) break;
+      // ---------------------------------------------------------------- the part's end
+      const int seg = cur.sb * a.Hkv + cur.s.h;
+      if (g == 0 && row == 0 && cur.unit0 == 0) {
+        int2 who = make_int2(0, 0);
+        if (!cur.complete) {
+          const int64_t end = run.u1 + (cur.s.units - cur.tiles);            // one behind the segment's last unit
+          who = make_int2((int)blockIdx.x, (int)((end * run.ctas - 1) / run.total));
+        }
+        a.info[seg] = who;
+      }
+      // A whole segment is answered here.  With the same rows in both groups, group 1 hands its share to
+      // group 0 through the CTA's record.
+      const bool both = !kPair && cur.complete && cur.tiles > 1;
+      const bool direct = cur.complete && (kPair || g == 0);
+      if (!kPair && cur.complete && g == 1 && !both) continue;
+      float* rec = a.part + (((size_t)blockIdx.x * 2 + (cur.unit0 == 0 ? 1 : 0)) * (kPair ? 1 : 2) + (kPair ? 0 : g)) *
+                                record_floats(kRowTile, D);
+      const int rr = (kPair ? g * 128 : 0) + row;
+      const bool live = j < cur.s.n;
+      const int head = cur.s.h * a.G + gr;
+      if (jobs > 0 && !warp_wait(&bars->pvdone[g], (job - 1) & 1u)) { ok = false; break; }
+      tc_fence_after();
+      const float* other = rec + record_floats(kRowTile, D);                 // group 1's record, for group 0
+      // the record of the last shared segment has been read
+      if (!kPair && g == 1 && !warp_wait(&bars->recfree, (shared & 1u) ^ 1u)) { ok = false; break; }
+      if (both && g == 0 && !warp_wait(&bars->recfull, shared & 1u)) { ok = false; break; }
+      float f = 1.f, f1 = 0.f;
+      if (direct && live) {                              // O relative to mw (and 2^kShift), the denominator to mz
+        float W = mw, Z = mz, den = l;
+        if (both) {
+          const float w1 = other[(size_t)kRowTile * D + rr], z1 = other[(size_t)kRowTile * (D + 1) + rr];
+          W = fmaxf(mw, w1);
+          Z = fmaxf(mz, z1);
+          den = l * exp2f(mz - Z) + other[(size_t)kRowTile * (D + 2) + rr] * exp2f(z1 - Z);
+          f1 = exp2f(w1 - W);
+        }
+        const bool none = Z == kNone && den == 0.f;
+        if (a.sinks) den += exp2f(a.sinks[head] * kLog2e - Z);
+        const float top = none ? 0.f : exp2f(W - Z - kShift) / den;
+        f = exp2f(mw - W) * top;
+        f1 *= top;
+      }
+      uint8_t* out = a.out + 2 * ((((size_t)cur.s.b * a.tok.Tq + j) * a.H + head) * D);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        __syncwarp();
+        if (jobs > 0) {
+          tmem_ld_32x32b_x32(o_addr + (uint32_t)c, o);
+          tmem_wait_ld();
+        } else {
+#pragma unroll
+          for (int q = 0; q < 32; ++q) o[q] = 0.f;
+        }
+        if (direct && live) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 8) {
+            float v[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = o[q + e] * f;
+            if (both) {
+              const float4 x0 = *reinterpret_cast<const float4*>(other + (size_t)rr * D + c + q);
+              const float4 x1 = *reinterpret_cast<const float4*>(other + (size_t)rr * D + c + q + 4);
+              v[0] = fmaf(x0.x, f1, v[0]); v[1] = fmaf(x0.y, f1, v[1]); v[2] = fmaf(x0.z, f1, v[2]); v[3] = fmaf(x0.w, f1, v[3]);
+              v[4] = fmaf(x1.x, f1, v[4]); v[5] = fmaf(x1.y, f1, v[5]); v[6] = fmaf(x1.z, f1, v[6]); v[7] = fmaf(x1.w, f1, v[7]);
+            }
+            uint4 y;
+            y.x = (uint32_t)f_to_bf16_bits(v[0]) | ((uint32_t)f_to_bf16_bits(v[1]) << 16);
+            y.y = (uint32_t)f_to_bf16_bits(v[2]) | ((uint32_t)f_to_bf16_bits(v[3]) << 16);
+            y.z = (uint32_t)f_to_bf16_bits(v[4]) | ((uint32_t)f_to_bf16_bits(v[5]) << 16);
+            y.w = (uint32_t)f_to_bf16_bits(v[6]) | ((uint32_t)f_to_bf16_bits(v[7]) << 16);
+            *reinterpret_cast<uint4*>(out + 2 * (c + q)) = y;
+          }
+        } else if (live) {
+#pragma unroll
+          for (int q = 0; q < 32; q += 4)
+            *reinterpret_cast<float4*>(rec + (size_t)rr * D + c + q) = make_float4(o[q], o[q + 1], o[q + 2], o[q + 3]);
+        }
+      }
+      if (jobs > 0) {
+        tc_fence_before();
+        mbar_arrive(&bars->ofree[g]);
+      }
+      if (!direct && live) {
+        rec[(size_t)kRowTile * D + rr] = mw;
+        rec[(size_t)kRowTile * (D + 1) + rr] = mz;
+        rec[(size_t)kRowTile * (D + 2) + rr] = l;
+      }
+      if (both) {
+        __threadfence_block();
+        mbar_arrive(g == 1 ? &bars->recfull : &bars->recfree);
+        ++shared;
+      }
+    }
+    if (!ok) set_device_error(a.err, kErrWaitTimeout);
+  } else {
+    // ------------------------------------------------------------------ conversion of K or V tiles
+    regs_dec<kRegsConvert>();
+    const bool is_v = warp >= 16;
+    const int w = warp & 3;
+    constexpr int kLanes = D / 16, kRowsPer = 32 / kLanes;    // lanes a row, rows a load of the warp
+    constexpr int kLoads = kSubs * 16 / (4 * kRowsPer);       // loads a thread and tile
+    const int c = lane % kLanes, r0 = w * kRowsPer + lane / kLanes;
+    uint8_t* tiles = sm + (is_v ? S::kOffV : S::kOffK);
+    uint64_t* full = is_v ? bars->vfull : bars->kfull;
+    uint64_t* freeb = is_v ? bars->vfree : bars->kfree;
+    const uint8_t* pool = is_v ? a.P.v : a.P.k;
+    bool ok = true;
+    bool more = next_part();
+    int i = 0;
+    uint32_t tile = 0;
+    int tmin = 0, tmax = 0;
+    if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
+    // page of the 16 keys that this lane (u < 8) looks up, of the tile to be loaded next
+    auto lookup = [&]() -> int32_t {
+      if (!more || lane >= kSubs) return -1;
+      return sub_page(a, pt.s, tile_pos(pt.s, pt.unit0 + i, kKeys) + 16 * lane, !is_v && w == 0);
+    };
+    uint4 x[kLoads];
+    auto load = [&](int32_t pg) {
+      const int pos = tile_pos(pt.s, pt.unit0 + i, kKeys);
+#pragma unroll
+      for (int it = 0; it < kLoads; ++it) {
+        const int r = it * 4 * kRowsPer + r0;
+        const int32_t p = __shfl_sync(0xffffffffu, pg, r >> 4);
+        x[it] = make_uint4(0u, 0u, 0u, 0u);
+        if (p >= 0)
+          x[it] = *reinterpret_cast<const uint4*>(
+              pool + (((size_t)p * a.Hkv + pt.s.h) * a.T.page + ((pos + r) & (a.T.page - 1))) * D + 16 * c);
+      }
+    };
+    int32_t pg = lookup();
+    bool masked = false;
+    if (more) {
+      load(pg);
+      const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+      masked = have != 0xFFu || !sees_all(a, tile_pos(pt.s, pt.unit0 + i, kKeys), tmin, tmax);
+    }
+    while (more) {
+      if (!warp_wait(&freeb[tile & 1], ((tile >> 1) & 1u) ^ 1u)) { ok = false; break; }
+      uint8_t* dst = tiles + (tile & 1) * S::kTileBytes;
+      if (is_v && masked) {
+        // some row does not see some key: NaN codes become 0 and are flagged for the rows that do
+#pragma unroll
+        for (int it = 0; it < kLoads; ++it) {
+          uint32_t* xw = reinterpret_cast<uint32_t*>(&x[it]);
+          uint32_t any = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t nb = nan_bytes(xw[q]);
+            any |= nb;
+            xw[q] &= ~((nb >> 7) * 0xFFu);
+          }
+          const uint32_t bal = __ballot_sync(0xffffffffu, any != 0);
+          // four rows to a byte
+          if (lane < kRowsPer / 4) {
+            uint32_t fl = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              fl |= ((bal >> ((4 * lane + q) * kLanes)) & ((1u << kLanes) - 1u)) ? 1u << q : 0u;
+            nans[(tile & 1) * 32 + (it * 4 * kRowsPer + w * kRowsPer) / 4 + lane] = (uint8_t)fl;
+          }
+        }
+      }
+#pragma unroll
+      for (int it = 0; it < kLoads; ++it) {
+        const int r = it * 4 * kRowsPer + r0;
+        const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+        uint4 y0, y1;
+        e4m3x4_f16(xw[0], y0.x, y0.y);
+        e4m3x4_f16(xw[1], y0.z, y0.w);
+        e4m3x4_f16(xw[2], y1.x, y1.y);
+        e4m3x4_f16(xw[3], y1.z, y1.w);
+        // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
+        uint8_t* at = dst + (c >> 2) * S::kHalf;
+        const int jx = (c & 3) * 2, up = (c >> 2) & 1;
+        *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
+        *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&full[tile & 1]);
+      ++tile;
+      if (++i == pt.tiles) {
+        i = 0;
+        more = next_part();
+        if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
+      }
+      if (more) {
+        pg = lookup();
+        load(pg);
+        const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
+        masked = have != 0xFFu || !sees_all(a, tile_pos(pt.s, pt.unit0 + i, kKeys), tmin, tmax);
+      }
+    }
+    if (!ok) set_device_error(a.err, kErrWaitTimeout);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kPair, int kW>
+cudaError_t launch_tc_as(const PagedAttendArgs& a, cudaStream_t s) {
+  auto kernel = paged_attend_tc_kernel<D, kPair, kW>;
+  // the warps' register split draws on what the block was launched with
+  cudaFuncAttributes attr;
+  cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
+  if (e != cudaSuccess) return e;
+  if (attr.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+  e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), TcShape<D>::kBytes);
+  if (e == cudaSuccess) e = launch_kernel(kernel, dim3(a.ctas), dim3(kThreads), TcShape<D>::kBytes, s, 0, a);
+  if (e == cudaSuccess)
+    e = launch_combine<D>(a, CombineShape{kPair ? 256 : 128, kKeys, 1, kPair ? 1 : 2, kShift}, s);
+  return e;
+}
+
+template <int D, bool kPair>
+cudaError_t launch_tc(const PagedAttendArgs& a, cudaStream_t s) {
+  return a.T.page == 16 ? launch_tc_as<D, kPair, 16>(a, s) : launch_tc_as<D, kPair, 32>(a, s);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+// Which kernel: the warp-level one for float32 activations and up to 16 query rows per KV head, tcgen05 above.
+PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms) {
+  PagedPlan p;
+  (void)n_max;
+  const int64_t rows = (int64_t)Tq * G;
+  p.path = act_fmt == CSA_FMT_F32 || rows <= 16 ? 1 : 2;
+  p.row_tile = p.path == 1 ? (rows <= 8 ? 8 : 16) : (rows <= 128 ? 128 : 256);
+  p.rb_max = (int)((rows + p.row_tile - 1) / p.row_tile);
+  p.ctas = num_sms;
+  size_t off = 256;                                           // the error word
+  p.info = off;
+  p.info_bytes = (size_t)B * p.rb_max * Hkv * sizeof(int2);
+  off = up256(off + p.info_bytes);
+  p.part = off;
+  p.part_bytes = (size_t)p.ctas * 2 * record_floats(p.path == 1 ? p.row_tile : 256, D) * 4;
+  p.total = up256(off + p.part_bytes);
+  return p;
+}
+
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, cudaStream_t s) {
+  if (p.path == 1) return launch_paged_attend_warp(a, p.row_tile, s);
+  if (a.D == 128) return p.row_tile == 256 ? launch_tc<128, true>(a, s) : launch_tc<128, false>(a, s);
+  return p.row_tile == 256 ? launch_tc<64, true>(a, s) : launch_tc<64, false>(a, s);
+}
+
+}  // namespace csa

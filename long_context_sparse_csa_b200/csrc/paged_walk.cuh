@@ -1,0 +1,228 @@
+// Shared by the two kernels of csa_paged_attend: how the work is cut and dealt, and how cut segments
+// are joined.
+//
+// A segment is one (sequence, block of query rows, KV head); a row is (token, head of the group).  Its
+// visible keys lie in tiles of a fixed number of positions; some tiles make a unit, and all segments'
+// units in order are dealt to the CTAs in equal runs.  A segment cut between CTAs leaves records (O,
+// its two running maxima, the denominator) that the combine kernel joins.  The cut depends on the
+// lengths alone, so results do not change from run to run.
+#pragma once
+
+#include "paged.h"
+
+namespace csa {
+
+namespace {
+
+constexpr float kNone = -3.0e38f;             // a running maximum before any key: finite, below every logit
+
+// One segment's tiles: [0, ta) and [tb, te) in units of 32 positions.
+struct Seg {
+  int b, rb, h;
+  int j0, n;                                  // first token of the block, tokens of the sequence answered
+  int start;
+  int ta, tb, te, tiles, units;
+};
+
+__device__ __forceinline__ int answered(const PagedAttendArgs& a, int b, int* start) {
+  const int64_t s = a.tok.start[b];
+  int n = a.tok.n_new ? a.tok.n_new[b] : a.tok.Tq;
+  n = n < 0 ? 0 : (n > a.tok.Tq ? a.tok.Tq : n);
+  if (s < 0 || s >= a.n_max) n = 0;
+  else if (s + n > a.n_max) n = (int)(a.n_max - s);
+  *start = n ? (int)s : 0;
+  return n;
+}
+
+// Fills the tile range of block rb (`tile` keys to a tile, `per` tiles to a unit).
+__device__ __forceinline__ void seg_range(const PagedAttendArgs& a, Seg& s, int row_tile, int tile, int per) {
+  const int r0 = s.rb * row_tile;
+  s.j0 = r0 / a.G;
+  if (s.j0 >= s.n) {
+    s.ta = s.tb = s.te = s.tiles = s.units = 0;
+    return;
+  }
+  int j1 = (r0 + row_tile - 1) / a.G;
+  j1 = j1 < s.n ? j1 : s.n - 1;
+  const int end = s.start + j1 + 1;
+  int lo = 0, fa = 0;
+  if (a.window > 0) {
+    lo = s.start + s.j0 + 1 - a.window;
+    lo = lo > 0 ? lo : 0;
+    fa = a.first < lo ? a.first : lo;
+  }
+  s.ta = (fa + tile - 1) / tile;
+  s.tb = lo / tile > s.ta ? lo / tile : s.ta;
+  s.te = (end + tile - 1) / tile;
+  if (s.tb > s.te) s.tb = s.te;
+  s.tiles = s.ta + s.te - s.tb;
+  s.units = (s.tiles + per - 1) / per;
+}
+
+__device__ __forceinline__ void seg_load(const PagedAttendArgs& a, Seg& s, int sb, int row_tile, int tile, int per) {
+  s.b = sb / a.rb_max;
+  s.rb = sb - s.b * a.rb_max;
+  s.n = answered(a, s.b, &s.start);
+  seg_range(a, s, row_tile, tile, per);
+}
+
+// This CTA's run of units [u0, u1) of all segments' units; *sb and *before: the (sequence, block) that
+// holds u0 and the units of the segments before it.  All threads of the CTA call it.
+struct Run {
+  int64_t u0, u1, before, total;
+  int sb, ctas;                               // CTAs with work: no more than units
+};
+
+__device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int64_t* scratch) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
+  const int n = a.T.B * a.rb_max;
+  const int each = (n + nt - 1) / nt;
+  int64_t sum = 0;
+  for (int i = tid * each; i < (tid + 1) * each && i < n; ++i) {
+    Seg s;
+    seg_load(a, s, i, row_tile, tile, per);
+    sum += s.units;
+  }
+  sum *= a.Hkv;
+  int64_t inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += up;
+  }
+  if (lane == 31) scratch[wid] = inc;
+  __syncthreads();
+  int64_t base = 0, total = 0;
+  for (int w = 0; w < (nt >> 5); ++w) {
+    const int64_t v = scratch[w];
+    if (w < wid) base += v;
+    total += v;
+  }
+  __syncthreads();
+  Run r;
+  r.total = total;
+  r.ctas = total < a.ctas ? (int)total : a.ctas;
+  r.u0 = r.u1 = 0;
+  if ((int)blockIdx.x < r.ctas) {
+    r.u0 = total * blockIdx.x / r.ctas;
+    r.u1 = total * (blockIdx.x + 1) / r.ctas;
+  }
+  int64_t at = base + inc - sum;
+  if (r.u0 < r.u1 && r.u0 >= at && r.u0 < at + sum) {
+    for (int i = tid * each;; ++i) {
+      Seg s;
+      seg_load(a, s, i, row_tile, tile, per);
+      const int64_t u = (int64_t)s.units * a.Hkv;
+      if (r.u0 < at + u) {
+        scratch[0] = i;
+        scratch[1] = at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  r.sb = (int)scratch[0];
+  r.before = scratch[1];
+  __syncthreads();
+  return r;
+}
+
+// Position of a walk over the units of a run.
+struct Walk {
+  Seg s;
+  int sb;
+  int unit;                                   // of the segment
+};
+
+__device__ __forceinline__ void walk_start(const PagedAttendArgs& a, Walk& w, const Run& r, int row_tile, int tile,
+                                           int per) {
+  w.sb = r.sb;
+  seg_load(a, w.s, w.sb, row_tile, tile, per);
+  const int64_t in = r.u0 - r.before;
+  w.s.h = (int)(in / w.s.units);
+  w.unit = (int)(in - (int64_t)w.s.h * w.s.units);
+}
+
+__device__ __forceinline__ void walk_next(const PagedAttendArgs& a, Walk& w, int row_tile, int tile, int per) {
+  if (++w.unit < w.s.units) return;
+  w.unit = 0;
+  if (++w.s.h < a.Hkv) return;
+  w.s.h = 0;
+  const int n = a.T.B * a.rb_max;
+  do {
+    ++w.sb;
+    if (w.sb >= n) return;                    // only behind the last unit
+    seg_load(a, w.s, w.sb, row_tile, tile, per);
+  } while (w.s.units == 0);
+}
+
+__device__ __forceinline__ int tile_pos(const Seg& s, int i, int tile) {
+  return (i < s.ta ? i : s.tb + (i - s.ta)) * tile;
+}
+
+// Floats of one partial record: O [rows][D], then mw, mz, l per row.
+__host__ __device__ constexpr size_t record_floats(int rows, int D) { return (size_t)rows * (D + 3); }
+
+// Record of CTA q's part of a segment that CTA `first` begins: a CTA's first segment may have begun
+// before it (record 0), its last may end after it (record 1); a segment that begins in it is record 1.
+__device__ __forceinline__ const float* record_of(const PagedAttendArgs& a, int q, int first, size_t floats) {
+  return a.part + ((size_t)q * 2 + (q == first ? 1 : 0)) * floats;
+}
+
+struct CombineShape {
+  int rows, tile, per;                        // rows of a block, keys of a tile, tiles of a unit
+  int groups;                                 // records of a part
+  float shift;                                // O is scaled by 2^shift
+};
+
+// Joins the records of the segments that were cut: a block per segment and four rows.
+template <int D>
+__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedAttendArgs a,
+                                                          const __grid_constant__ CombineShape cs) {
+  const int seg = blockIdx.x, rows = cs.rows;
+  Seg s;
+  seg_load(a, s, seg / a.Hkv, rows, cs.tile, cs.per);
+  s.h = seg % a.Hkv;
+  const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
+  const int R = s.rb * rows + r, j = R / a.G, gr = R - j * a.G;
+  if (s.units == 0 || j >= s.n) return;
+  const int2 who = a.info[seg];
+  if (who.x >= who.y) return;                                 // one CTA had all of it
+  const size_t floats = record_floats(rows, D);
+  float W = kNone, Z = kNone;
+#pragma unroll 4
+  for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
+    const int q = i / cs.groups, g = i - q * cs.groups;
+    const float* st = record_of(a, q, who.x, floats * cs.groups) + g * floats + (size_t)rows * D + r;
+    W = fmaxf(W, st[0]);
+    Z = fmaxf(Z, st[rows]);
+  }
+  float L = 0.f;
+  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
+    const int q = i / cs.groups, g = i - q * cs.groups;
+    const float* rec = record_of(a, q, who.x, floats * cs.groups) + g * floats;
+    const float* st = rec + (size_t)rows * D + r;
+    const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
+    const float f = exp2f(st[0] - W);
+    L += st[2 * rows] * exp2f(st[rows] - Z);
+    v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+  }
+  const int head = s.h * a.G + gr;
+  if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
+  const float f = Z == kNone && !(L != L) ? 0.f : exp2f(W - Z - cs.shift) / L;
+  const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+  const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
+  store_act4(a.out + at * act_bytes(a.act_fmt), a.act_fmt, 0, out);
+}
+
+template <int D>
+cudaError_t launch_combine(const PagedAttendArgs& a, const CombineShape& cs, cudaStream_t s) {
+  return launch_kernel(paged_combine_kernel<D>, dim3((unsigned)(a.T.B * a.rb_max * a.Hkv), cs.rows / 4), dim3(D), 0, s,
+                       0, a, cs);
+}
+
+}  // namespace
+}  // namespace csa

@@ -318,6 +318,18 @@ def test_long_sequences_split_over_the_gpu():
         _close(*_attend(cache, table, [n - 1], None, 1, H, act, rng=rng))
 
 
+@pytest.mark.parametrize("Tq,H,Hkv,D", [(7, 32, 4, 128), (20, 8, 4, 64), (33, 16, 2, 64)])
+def test_ctas_with_several_short_segments(Tq, H, Hkv, D):
+    """More segments than SMs, of odd and even numbers of key tiles, cut at any place."""
+    rng = np.random.default_rng(Tq)
+    B, page = 44, 32
+    start = rng.integers(0, 1500, B)
+    held = [-(-(s + Tq) // page) for s in start]
+    cache = Cache(rng, sum(held), Hkv, page, D)
+    table, _ = _table(rng, B, max(held), cache.N, held)
+    _close(*_attend(cache, table, start, rng.integers(0, Tq + 1, B), Tq, H, rng=rng))
+
+
 def test_offsets_behind_2_31_bytes():
     """A pool of more than 2^32 bytes: the pages in use are its last."""
     Hkv, page, D, N = 8, 128, 128, 36000
