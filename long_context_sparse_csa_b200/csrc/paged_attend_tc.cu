@@ -15,7 +15,7 @@
 // very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when a
 // tile exceeds it by more than 8 (then O is rescaled in tensor memory), so P stays below 2^15.
 //
-// Roles (640 threads): warp 0 issues the products; warps 4-7 and 8-11 are the two groups' softmax, a
+// Roles (640 threads): warp 0 issues the products; warp 1 looks up the tiles' pages and scales; warps 4-7 and 8-11 are the two groups' softmax, a
 // thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles: 16-byte loads of codes, one tile ahead in
 // registers, to f16 in the 128-byte swizzle (two stages each).  A job is one (tile, group).  With more
 // than 128 rows (kPair) the groups take different rows of the same tile; otherwise the same rows of
@@ -35,15 +35,27 @@ using namespace sm100;
 constexpr int kKeys = 128;
 constexpr int kThreads = 640;
 constexpr int kSubs = kKeys / 16;
+constexpr int kMeta = 8;                        // tiles looked up ahead, four at a time
 constexpr float kShift = 7.f, kMargin = 8.f;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsConvert = 88, kRegsIssue = 48;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsConvert = 72, kRegsIssue = 80;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
 
 struct __align__(8) TcBars {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
   uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], ofree[2];
   uint64_t recfull, recfree;
+  uint64_t mfull[kMeta], mfree[kMeta];
   uint32_t tmem_base;
+};
+
+// What the other roles need of a key tile, looked up ahead by one warp.
+struct TileMeta {
+  int32_t page[kSubs];                        // page of each 16 keys, -1: none
+  float ks[kSubs], lv[kSubs];                 // key scale, log2 of the value scale
+  int pos, h;                                 // first position, KV head
+  int index;                                  // number of the tile in its part
+  int whole;                                  // every row of the block sees every key
+  uint32_t have;                              // bits: the 16 keys have a page
 };
 
 // A CTA's part of a segment.
@@ -76,7 +88,8 @@ struct TcShape {
   static constexpr size_t kOffNan = kOffCq + 2 * 128 * 4;     // [2 stages][32] NaN flags of V's rows, four to a byte
   static constexpr size_t kOffBars = kOffNan + 64;
   static constexpr size_t kOffScan = kOffBars + (sizeof(TcBars) + 7) / 8 * 8;
-  static constexpr size_t kOffWalk = kOffScan + (kThreads / 32) * 8;
+  static constexpr size_t kOffMeta = kOffScan + (kThreads / 32) * 8;
+  static constexpr size_t kOffWalk = kOffMeta + kMeta * sizeof(TileMeta);
   static constexpr size_t kBytes = 1024 + kOffWalk + (kThreads / 32) * sizeof(WarpWalk);
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
@@ -170,17 +183,6 @@ __device__ __forceinline__ bool parts_next(const PagedAttendArgs& a, Parts& p, P
   return true;
 }
 
-// Page of the 16 positions from pos on, -1 where there is none (or nothing of the sequence).
-__device__ __forceinline__ int32_t sub_page(const PagedAttendArgs& a, const Seg& s, int pos, bool report) {
-  if (pos >= s.start + s.n) return -1;
-  const int32_t g = a.T.table[(size_t)s.b * a.T.cap + (pos >> a.T.page_log2)];
-  if (g >= a.T.n_pages) {
-    if (report) set_device_error(a.err, kErrPage);
-    return -1;
-  }
-  return g < 0 ? -1 : g;
-}
-
 // First and last position of the block's tokens.
 __device__ __forceinline__ void row_span(const PagedAttendArgs& a, const Seg& s, int row_tile, int* tmin, int* tmax) {
   const int j1 = (s.rb * row_tile + row_tile - 1) / a.G;
@@ -200,7 +202,7 @@ template <int D, bool kPair, int kW>
 __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __grid_constant__ PagedAttendArgs a) {
   using S = TcShape<D>;
   constexpr int kRowTile = kPair ? 256 : 128;
-  constexpr int kHalves = D / 64, kScales = kKeys / kW;
+  constexpr int kHalves = D / 64;
   extern __shared__ uint8_t tc_smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(tc_smem_raw) + 1023) & ~uintptr_t(1023));
   float* cqs = reinterpret_cast<float*>(sm + S::kOffCq);
@@ -222,6 +224,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     }
     mbar_init(&bars->recfull, 128);
     mbar_init(&bars->recfree, 128);
+    for (int i = 0; i < kMeta; ++i) {
+      mbar_init(&bars->mfull[i], kSubs);
+      mbar_init(&bars->mfree[i], 9 + (kPair ? 8 : 4));   // a lane of every warp that reads the entry
+    }
     fence_barrier_init();
   }
   const Run run = find_run(a, kRowTile, kKeys, 1, reinterpret_cast<int64_t*>(sm + S::kOffScan));
@@ -234,6 +240,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  TileMeta* metas = reinterpret_cast<TileMeta*>(sm + S::kOffMeta);
+  const int64_t run_tiles = run.u1 - run.u0;
   WarpWalk& walk = reinterpret_cast<WarpWalk*>(sm + S::kOffWalk)[warp];
   Part& pt = walk.next;
   if (lane == 0) parts_start(a, walk.parts, run, kRowTile);
@@ -253,50 +261,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       const uint64_t q_desc = desc_kmajor_sw128(smem_u32(sm));
       const uint64_t k_desc = desc_kmajor_sw128(smem_u32(sm + S::kOffK));
       const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(sm + S::kOffV), S::kHalf, 1024u);
+      // Jobs in order, n = 0, 1, ...; QK of job n, then PV of job n - 1 (before it, where both are the same
+      // group's: a part of an odd number of tiles ended).  Bit g of the masks belongs to group g.
+      const uint32_t jobs = (uint32_t)run_tiles * (kPair ? 2u : 1u);
       bool ok = true;
-      uint32_t jobs[2] = {0, 0}, parts_of[2] = {0, 0}, opens[2] = {0, 0};    // of each group, so far
-      uint32_t ktile = 0;                                                    // tiles so far (K and V)
-      // the product P V that is still to be issued
-      bool pend = false;
-      int pg = 0;
-      uint32_t ptile = 0;
-      bool pfirst = false, plast_use = false;
-      uint32_t pjob = 0;
-      auto pv = [&]() {
-        if (!pend) return;
-        pend = false;
-        ok = ok && mbar_wait(&bars->vfull[ptile & 1], (ptile >> 1) & 1u);
-        if (ok && pfirst) {                              // O of the group's last segment has been read
-          ok = mbar_wait(&bars->ofree[pg], (opens[pg] & 1u) ^ 1u);
-          ++opens[pg];
+      uint32_t jpar = 0, qpar = 0, opar = 0, begun = 0;      // parities of its jobs, parts' queries, parts' O; any job yet
+      bool pend = false, pfirst = false;
+      uint32_t pg = 0, pn = 0;
+#pragma unroll 1
+      for (uint32_t n = 0; n <= jobs && ok; ++n) {
+        const uint32_t tile = kPair ? n >> 1 : n, st = tile & 1u;
+        const bool have = n < jobs;
+        uint32_t g = 2;
+        bool first = false;
+        if (have) {
+          ok = mbar_wait(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u);
+          const int idx = metas[tile % kMeta].index;
+          if (!kPair || (n & 1u)) mbar_arrive(&bars->mfree[tile % kMeta]);
+          g = (kPair ? n : (uint32_t)idx) & 1u;
+          first = kPair ? idx == 0 : idx < 2;
         }
-        ok = ok && mbar_wait(&bars->pfull[pg], pjob & 1u);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t vd = v_desc + (uint64_t)((ptile & 1) * (S::kTileBytes >> 4));
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_f16_ts(tmem + 256u + (uint32_t)(pg * D), tmem + (uint32_t)(pg * 128 + 64 + 8 * kk), vd + (uint64_t)((kk * 2048) >> 4),
-                      idesc_o, (pfirst && kk == 0) ? 0u : 1u);
-        umma_commit(&bars->pvdone[pg]);
-        if (plast_use) umma_commit(&bars->vfree[ptile & 1]);
-      };
-      while (ok && parts_next(a, walk.parts, pt, kRowTile)) {
-        for (int i = 0; i < pt.tiles && ok; ++i, ++ktile) {
-          const uint32_t st = ktile & 1u;
-          ok = mbar_wait(&bars->kfull[st], (ktile >> 1) & 1u);
-          for (int u = 0; u < (kPair ? 2 : 1) && ok; ++u) {
-            const int g = kPair ? u : (i & 1);
-            const bool first = kPair ? i == 0 : i < 2;
-            // the same group twice in a row (a part of an odd number of tiles ended): its P comes first
-            if (pend && pg == g) pv();
-            if (first) {
-              ok = mbar_wait(&bars->qfull[g], parts_of[g] & 1u);
-              ++parts_of[g];
+#pragma unroll 1
+        for (int step = pend && pg == g ? 0 : 1; step < 3 && ok; ++step) {
+          if (step == 1) {
+            if (!have) continue;
+            ok = mbar_wait(&bars->kfull[st], (tile >> 1) & 1u);
+            if (ok && first) {
+              ok = mbar_wait(&bars->qfull[g], (qpar >> g) & 1u);
+              qpar ^= 1u << g;
             }
             // the group's last P has been read (its columns are S's)
-            if (ok && jobs[g] > 0) ok = mbar_wait(&bars->pvdone[g], (jobs[g] - 1) & 1u);
+            if (ok && ((begun >> g) & 1u)) ok = mbar_wait(&bars->pvdone[g], ((jpar >> g) & 1u) ^ 1u);
             if (!ok) break;
+            begun |= 1u << g;
+            jpar ^= 1u << g;
             tc_fence_after();
             const uint64_t qd = q_desc + (uint64_t)(g * (S::kTileBytes >> 4));
             const uint64_t kd = k_desc + (uint64_t)(st * (S::kTileBytes >> 4));
@@ -304,26 +302,103 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             for (int h = 0; h < kHalves; ++h)
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                umma_f16(tmem + (uint32_t)(g * 128), qd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk),
+                umma_f16(tmem + g * 128u, qd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk),
                          kd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk), idesc_s, (h | kk) ? 1u : 0u);
             umma_commit(&bars->sfull[g]);
-            const bool last_use = !kPair || u == 1;
-            if (last_use) umma_commit(&bars->kfree[st]);
-            pv();
-            pend = true;
-            pg = g;
-            ptile = ktile;
-            pfirst = first;
-            plast_use = last_use;
-            pjob = jobs[g]++;
+            if (!kPair || (n & 1u)) umma_commit(&bars->kfree[st]);
+          } else if (pend) {
+            pend = false;
+            const uint32_t ptile = kPair ? pn >> 1 : pn;
+            ok = mbar_wait(&bars->vfull[ptile & 1], (ptile >> 1) & 1u);
+            if (ok && pfirst) {                            // O of the group's last part has been read
+              ok = mbar_wait(&bars->ofree[pg], ((opar >> pg) & 1u) ^ 1u);
+              opar ^= 1u << pg;
+            }
+            // jpar has moved on by the job itself, and once more if its group's next QK has been issued: it has not
+            ok = ok && mbar_wait(&bars->pfull[pg], ((jpar >> pg) & 1u) ^ 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t vd = v_desc + (uint64_t)((ptile & 1) * (S::kTileBytes >> 4));
+            const uint32_t od = tmem + 256u + pg * (uint32_t)D, pd = tmem + pg * 128u + 64u;
+#pragma unroll
+            for (int kk = 0; kk < kKeys / 16; ++kk)
+              umma_f16_ts(od, pd + 8u * kk, vd + (uint64_t)((kk * 2048) >> 4), idesc_o, (pfirst && kk == 0) ? 0u : 1u);
+            umma_commit(&bars->pvdone[pg]);
+            if (!kPair || (pn & 1u)) umma_commit(&bars->vfree[ptile & 1]);
           }
         }
+        pend = have;
+        pg = g;
+        pn = n;
+        pfirst = first;
       }
-      if (ok) pv();
       if (!ok) set_device_error(a.err, kErrWaitTimeout);
-      // nothing of this thread is in flight when tensor memory is released
-      for (int g = 0; g < 2; ++g)
-        if (jobs[g] > 0) mbar_wait(&bars->pvdone[g], (jobs[g] - 1) & 1u);
+      // nothing of this thread is in flight when tensor memory is released: the last PV of each group, or QK
+      for (uint32_t g = 0; g < 2; ++g)
+        if ((begun >> g) & 1u) mbar_wait(&bars->pvdone[g], ((jpar >> g) & 1u) ^ 1u);
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- pages and scales, four tiles at a time
+      bool ok = true;
+      int i = 0, tmin = 0, tmax = 0;
+      bool more = next_part();
+      if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
+      for (int64_t n0 = 0; n0 < run_tiles; n0 += 4) {
+        int pos = 0, h = 0, b = 0, limit = 0, index = 0;
+        bool all = false;
+        for (int k = 0; k < 4 && n0 + k < run_tiles; ++k) {
+          if ((lane >> 3) == k) {
+            const int p0 = tile_pos(pt.s, pt.unit0 + i, kKeys);
+            all = sees_all(a, p0, tmin, tmax);
+            pos = p0;
+            h = pt.s.h;
+            index = i;
+            b = pt.s.b;
+            limit = pt.s.start + pt.s.n;
+          }
+          __syncwarp();
+          if (++i == pt.tiles) {
+            i = 0;
+            more = next_part();
+            if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
+          }
+        }
+        const bool mine = n0 + (lane >> 3) < run_tiles;
+        const int u = lane & 7, at = pos + 16 * u;
+        int32_t pg = -1;
+        if (mine && at < limit) pg = a.T.table[(size_t)b * a.T.cap + (at >> a.T.page_log2)];
+        if (pg >= a.T.n_pages) {
+          set_device_error(a.err, kErrPage);
+          pg = -1;
+        }
+        if (pg < 0) pg = -1;
+        float ks = 0.f, vs = 1.f;
+        if (pg >= 0) {
+          const size_t gh = (size_t)pg * a.Hkv + h;
+          ks = a.P.ks[gh];
+          vs = a.P.vs[gh];
+        }
+        const uint32_t have = (__ballot_sync(0xffffffffu, pg >= 0) >> (lane & 24)) & 0xFFu;
+        const int e = (int)((n0 + (lane >> 3)) & (kMeta - 1));
+        bool w = true;
+        if (mine) w = mbar_wait(&bars->mfree[e], (uint32_t)(((n0 + (lane >> 3)) / kMeta) & 1) ^ 1u);
+        if (!__all_sync(0xffffffffu, w)) { ok = false; break; }
+        if (mine) {
+          TileMeta& m = metas[e];
+          m.page[u] = pg;
+          m.ks[u] = ks;
+          m.lv[u] = (float)((int)((__float_as_uint(vs) >> 23) & 255u) - 127);
+          if (u == 0) {
+            m.pos = pos;
+            m.h = h;
+            m.index = index;
+            m.whole = all && have == 0xFFu;
+            m.have = have;
+          }
+          mbar_arrive(&bars->mfull[e]);
+        }
+        __syncwarp();
+      }
+      if (!ok) set_device_error(a.err, kErrWaitTimeout);
     }
     __syncwarp();
   } else if (warp < 12) {
@@ -377,180 +452,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       mbar_arrive(&bars->qfull[g]);
     };
 
-    bool more = next_part();
-    if (more && (kPair || pt.tiles > g)) load_q(pt);
-    while (more && ok) {
-      __syncwarp();
-      if (lane == 0) walk.cur = walk.next;
-      __syncwarp();
-      const Part& cur = walk.cur;
-      const int jobs = kPair ? cur.tiles : (cur.tiles - g + 1) / 2;
-      float mw = kNone, mz = kNone, l = 0.f;
-      const int R = cur.s.rb * kRowTile + (kPair ? g * 128 : 0) + row, j = R / a.G, gr = R - j * a.G;
-      const int t = j < cur.s.n ? cur.s.start + j : -1;
-      int tmin, tmax;
-      row_span(a, cur.s, kRowTile, &tmin, &tmax);
-      const float cq = cqs[g * 128 + row];
-      // lane u < 8: page and scales of the tile's u-th 16 keys, one job ahead
-      auto tile_of = [&](int i) { return kPair ? i : 2 * i + g; };
-      auto scales = [&](int i, float& ks, float& lv) {
-        ks = 0.f;
-        lv = 0.f;
-        bool there = false;
-        if (i < jobs && lane < kSubs) {
-          const int pos = tile_pos(cur.s, cur.unit0 + tile_of(i), kKeys) + 16 * lane;
-          const int32_t pg = sub_page(a, cur.s, pos, false);
-          if (pg >= 0) {
-            const size_t gh = (size_t)pg * a.Hkv + cur.s.h;
-            there = true;
-            ks = a.P.ks[gh];
-            lv = (float)((int)((__float_as_uint(a.P.vs[gh]) >> 23) & 255u) - 127);
-          }
-        }
-        return __ballot_sync(0xffffffffu, there) & 0xFFu;
-      };
-      float nks, nlv;
-      uint32_t nhave = scales(0, nks, nlv);
-      for (int i = 0; i < jobs && ok; ++i, ++job) {
-        const float ks = nks, lvs = nlv;
-        const uint32_t have = nhave;
-        nhave = scales(i + 1, nks, nlv);
-        const int ti = tile_of(i);
-        const int pos = tile_pos(cur.s, cur.unit0 + ti, kKeys);
-        const bool whole = have == 0xFFu && sees_all(a, pos, tmin, tmax);
-        const uint32_t tile = tile0 + (uint32_t)ti;
-        if (!warp_wait(&bars->sfull[g], job & 1u)) { ok = false; break; }
-        if (!whole && !warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u)) { ok = false; break; }   // the NaN flags
-        tc_fence_after();
-        // Half of the tile's scores (64 columns) in registers at a time: the maxima of the first half, then of
-        // the second; P of the second while it is there; the first half read once more.  P takes columns
-        // [64, 128) of S, so that what is written has always been read.
-        float x[64];
-        auto fetch = [&](int hb) {
-          __syncwarp();
-          tmem_ld_32x32b_x32(s_addr + 64u * hb, x);
-          tmem_ld_32x32b_x32(s_addr + 64u * hb + 32u, x + 32);
-          tmem_wait_ld();
-        };
-        auto hide = [&](int hb) {                        // masked scores to -inf, NaN where V's row has one
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int q = 2 * hb + k, p0 = pos + 32 * q;
-            uint32_t m = bits_to(t - p0);
-            if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
-            const uint32_t hv = (have >> (2 * q)) & 3u;
-            m &= ((hv & 1u) ? 0xFFFFu : 0u) | ((hv & 2u) ? 0xFFFF0000u : 0u);
-            if (t < 0) m = 0u;
-            const uint2 nb = *reinterpret_cast<const uint2*>(nans + (tile & 1) * 32 + 8 * q);
-            if (nb.x | nb.y) {
-              uint32_t nan32 = 0;
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                nan32 |= ((nb.x >> (8 * c)) & 15u) << (4 * c) | ((nb.y >> (8 * c)) & 15u) << (16 + 4 * c);
-#pragma unroll
-              for (int c = 0; c < 32; ++c)
-                if ((nan32 >> c) & 1u) x[32 * k + c] = __int_as_float(0x7fffffff);
-            }
-#pragma unroll
-            for (int c = 0; c < 32; ++c) x[32 * k + c] = (m >> c) & 1u ? x[32 * k + c] : -INFINITY;
-          }
-        };
-        float fs[kScales], ls[kScales];                  // logit factor and log2 of the value scale per kW columns
-#pragma unroll
-        for (int u = 0; u < kScales; ++u) {
-          fs[u] = fmaxf(fminf(__shfl_sync(0xffffffffu, ks, u * (kW / 16)) * cq, 3.0e38f), 1.2e-38f);
-          ls[u] = __shfl_sync(0xffffffffu, lvs, u * (kW / 16));
-        }
-        float cz = -INFINITY, cw = -INFINITY;
-        auto maxima = [&](int hb) {
-#pragma unroll
-          for (int v = 0; v < 64 / kW; ++v) {
-            const int u = hb * (64 / kW) + v;
-            float t0 = fmaxf(x[kW * v], x[kW * v + 1]), t1 = fmaxf(x[kW * v + 2], x[kW * v + 3]);
-#pragma unroll
-            for (int c = 4; c < kW; c += 4) {
-              t0 = fmaxf(t0, fmaxf(x[kW * v + c], x[kW * v + c + 1]));
-              t1 = fmaxf(t1, fmaxf(x[kW * v + c + 2], x[kW * v + c + 3]));
-            }
-            const float zt = fmaxf(t0, t1) * fs[u];
-            cz = fmaxf(cz, zt);
-            cw = fmaxf(cw, zt + ls[u]);
-          }
-        };
-        fetch(0);
-        if (!whole) hide(0);
-        maxima(0);
-        fetch(1);
-        if (!whole) hide(1);
-        maxima(1);
-        const bool move = cw > mw + kMargin || cz > mz + 40.f;
-        if (__any_sync(0xffffffffu, move)) {
-          const float nw = move ? fmaxf(mw, cw) : mw, nz = move ? fmaxf(mz, cz) : mz;
-          const float al = ex2(mw - nw);
-          l *= ex2(mz - nz);
-          mw = nw;
-          mz = nz;
-          if (i > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float o[16];
-              tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
-              tmem_wait_ld();
-              uint32_t ow[16];
-#pragma unroll
-              for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
-              tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
-            }
-          }
-        }
-        auto weigh = [&](int hb) {
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            uint32_t p[16];
-#pragma unroll
-            for (int v = 0; v < 32 / kW; ++v) {
-              const int u = (2 * hb + k) * (32 / kW) + v;
-              const float* xs = x + 32 * k + kW * v;
-              const float b = ls[u] - mw + kShift;
-              const float back = mw - mz - ls[u] - kShift;
-              if (back > 80.f) {
-                float apart = 0.f;
-#pragma unroll
-                for (int c = 0; c < kW; ++c) apart += ex2(xs[c] * fs[u] - mz);
-                l += apart;
-              }
-              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-              const float2 f2 = make_float2(fs[u], fs[u]), b2 = make_float2(b, b);
-#pragma unroll
-              for (int c = 0; c < kW; c += 4) {
-                float2 y0 = fma2(make_float2(xs[c], xs[c + 1]), f2, b2);
-                float2 y1 = fma2(make_float2(xs[c + 2], xs[c + 3]), f2, b2);
-                y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
-                s0 = add2(s0, y0);
-                s1 = add2(s1, y1);
-                p[(kW * v + c) / 2] = pack_f16x2(y0.x, y0.y);
-                p[(kW * v + c) / 2 + 1] = pack_f16x2(y1.x, y1.y);
-              }
-              s0 = add2(s0, s1);
-              if (!(back > 80.f)) l = fmaf(s0.x + s0.y, ex2(back), l);
-            }
-            __syncwarp();                                // rows may have parted above
-            tmem_st_32x32b_x16(s_addr + 64u + 32u * hb + 16u * k, p);
-          }
-        };
-        weigh(1);
-        fetch(0);
-        if (!whole) hide(0);
-        weigh(0);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        mbar_arrive(&bars->pfull[g]);
-      }
-      tile0 += (uint32_t)cur.tiles;
-      // the next part's queries, while the last product runs
-      more = next_part();
-      if (ok && more && (kPair || pt.tiles > g)) load_q(pt);
-      if (!ok) break;
+    // Per part: its tiles; then the next part's queries, while the last product runs; then its end.
+    Part& cur = walk.cur;
+    float mw = kNone, mz = kNone, l = 0.f, cq = 0.f;
+    int jobs = 0, j = 0, gr = 0, t = -1;
+    // The end of the part `cur`: its answer, or its record.
+    auto finish = [&]() {
       // ---------------------------------------------------------------- the part's end
       const int seg = cur.sb * a.Hkv + cur.s.h;
       if (g == 0 && row == 0 && cur.unit0 == 0) {
@@ -565,18 +472,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       // group 0 through the CTA's record.
       const bool both = !kPair && cur.complete && cur.tiles > 1;
       const bool direct = cur.complete && (kPair || g == 0);
-      if (!kPair && cur.complete && g == 1 && !both) continue;
+      if (!kPair && cur.complete && g == 1 && !both) return true;
       float* rec = a.part + (((size_t)blockIdx.x * 2 + (cur.unit0 == 0 ? 1 : 0)) * (kPair ? 1 : 2) + (kPair ? 0 : g)) *
                                 record_floats(kRowTile, D);
       const int rr = (kPair ? g * 128 : 0) + row;
       const bool live = j < cur.s.n;
       const int head = cur.s.h * a.G + gr;
-      if (jobs > 0 && !warp_wait(&bars->pvdone[g], (job - 1) & 1u)) { ok = false; break; }
+      if (jobs > 0 && !warp_wait(&bars->pvdone[g], (job - 1) & 1u)) return false;
       tc_fence_after();
       const float* other = rec + record_floats(kRowTile, D);                 // group 1's record, for group 0
       // the record of the last shared segment has been read
-      if (!kPair && g == 1 && !warp_wait(&bars->recfree, (shared & 1u) ^ 1u)) { ok = false; break; }
-      if (both && g == 0 && !warp_wait(&bars->recfull, shared & 1u)) { ok = false; break; }
+      if (!kPair && g == 1 && !warp_wait(&bars->recfree, (shared & 1u) ^ 1u)) return false;
+      if (both && g == 0 && !warp_wait(&bars->recfull, shared & 1u)) return false;
       float f = 1.f, f1 = 0.f;
       if (direct && live) {                              // O relative to mw (and 2^kShift), the denominator to mz
         float W = mw, Z = mz, den = l;
@@ -644,6 +551,182 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         mbar_arrive(g == 1 ? &bars->recfull : &bars->recfree);
         ++shared;
       }
+      return true;
+    };
+
+    bool more = next_part(), any = false;
+    for (;;) {
+      if (more && (kPair || pt.tiles > g)) load_q(pt);
+      if (any && !finish()) { ok = false; break; }
+      if (!more) break;
+      any = true;
+      __syncwarp();
+      if (lane == 0) cur = pt;
+      __syncwarp();
+      jobs = kPair ? cur.tiles : (cur.tiles - g + 1) / 2;
+      mw = mz = kNone;
+      l = 0.f;
+      const int R = cur.s.rb * kRowTile + (kPair ? g * 128 : 0) + row;
+      j = R / a.G;
+      gr = R - j * a.G;
+      t = j < cur.s.n ? cur.s.start + j : -1;
+      cq = cqs[g * 128 + row];
+      for (int i = 0; i < jobs && ok; ++i, ++job) {
+        const uint32_t tile = tile0 + (uint32_t)(kPair ? i : 2 * i + g);
+        if (!warp_wait(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { ok = false; break; }
+        const TileMeta& meta = metas[tile % kMeta];
+        const int pos = meta.pos;
+        const bool whole = meta.whole != 0;
+        if (!warp_wait(&bars->sfull[g], job & 1u)) { ok = false; break; }
+        if (!whole && !warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u)) { ok = false; break; }   // the NaN flags
+        tc_fence_after();
+        if (!whole) {
+          // scores that the row does not see become -inf, and NaN where the key's V row has a NaN code
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            float y[32];
+            __syncwarp();
+            tmem_ld_32x32b_x32(s_addr + 32u * q, y);
+            tmem_wait_ld();
+            const int p0 = pos + 32 * q;
+            uint32_t m = bits_to(t - p0);
+            if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
+            const uint32_t hv = (meta.have >> (2 * q)) & 3u;
+            m &= ((hv & 1u) ? 0xFFFFu : 0u) | ((hv & 2u) ? 0xFFFF0000u : 0u);
+            if (t < 0) m = 0u;
+            const uint2 nb = *reinterpret_cast<const uint2*>(nans + (tile & 1) * 32 + 8 * q);
+            uint32_t nan32 = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              nan32 |= ((nb.x >> (8 * c)) & 15u) << (4 * c) | ((nb.y >> (8 * c)) & 15u) << (16 + 4 * c);
+            nan32 &= m;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              if (!((m >> c) & 1u)) y[c] = -INFINITY;
+              if ((nan32 >> c) & 1u) y[c] = __int_as_float(0x7fffffff);
+            }
+            tmem_st_32x32b_x32(s_addr + 32u * q, y);
+          }
+          tmem_wait_st();
+        }
+        // Half of the tile's scores (64 columns) in registers at a time: the maxima of the first half, then of
+        // the second; P of the second while it is there; the first half read once more.  P takes columns
+        // [64, 128) of S, so that what is written has always been read.  The loops stay rolled: unrolled, the
+        // roles' code does not fit the instruction caches (2,050 us instead of the present time for the chunk
+        // of 2,048 tokens behind 14,336).
+        constexpr int kU = 64 / kW;                      // scales in a half
+        float x[64], fs[kU], ls[kU];                     // logit factor and log2 of the value scale per kW columns
+        auto scales = [&](int hb) {
+#pragma unroll
+          for (int v = 0; v < kU; ++v) {
+            const int u = 4 * hb + v * (kW / 16);
+            fs[v] = fmaxf(fminf(meta.ks[u] * cq, 3.0e38f), 1.2e-38f);
+            ls[v] = meta.lv[u];
+          }
+        };
+        float cz = -INFINITY, cw = -INFINITY;
+#pragma unroll 1
+        for (int hb = 0; hb < 2; ++hb) {
+          tmem_ld_32x32b_x32(s_addr + 64u * hb, x);
+          tmem_ld_32x32b_x32(s_addr + 64u * hb + 32u, x + 32);
+          scales(hb);
+          tmem_wait_ld();
+#pragma unroll
+          for (int v = 0; v < kU; ++v) {
+            float t0 = fmaxf(x[kW * v], x[kW * v + 1]), t1 = fmaxf(x[kW * v + 2], x[kW * v + 3]);
+#pragma unroll
+            for (int c = 4; c < kW; c += 4) {
+              t0 = fmaxf(t0, fmaxf(x[kW * v + c], x[kW * v + c + 1]));
+              t1 = fmaxf(t1, fmaxf(x[kW * v + c + 2], x[kW * v + c + 3]));
+            }
+            const float zt = fmaxf(t0, t1) * fs[v];
+            cz = fmaxf(cz, zt);
+            cw = fmaxf(cw, zt + ls[v]);
+          }
+        }
+        const bool move = cw > mw + kMargin || cz > mz + 40.f;
+        if (__any_sync(0xffffffffu, move)) {
+          const float nw = move ? fmaxf(mw, cw) : mw, nz = move ? fmaxf(mz, cz) : mz;
+          const float al = ex2(mw - nw);
+          l *= ex2(mz - nz);
+          mw = nw;
+          mz = nz;
+          if (i > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              float o[16];
+              tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
+              tmem_wait_ld();
+              uint32_t ow[16];
+#pragma unroll
+              for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
+              tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
+            }
+          }
+        }
+        // denominators whose factor is out of range: their exponentials apart
+        const float back0 = mw - mz - kShift;
+        bool far = false;
+#pragma unroll
+        for (int u = 0; u < kSubs; ++u) far |= back0 - meta.lv[u] > 80.f;
+        if (__any_sync(0xffffffffu, far)) {
+#pragma unroll 1
+          for (int q = 0; q < 8; ++q) {
+            float y[16];
+            __syncwarp();
+            tmem_ld_32x32b_x16(s_addr + 16u * q, y);
+            tmem_wait_ld();
+            const float fq = fmaxf(fminf(meta.ks[q] * cq, 3.0e38f), 1.2e-38f);
+            if (back0 - meta.lv[q] > 80.f) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) l += ex2(y[c] * fq - mz);
+            }
+          }
+          __syncwarp();
+        }
+#pragma unroll 1
+        for (int hb = 1; hb >= 0; --hb) {
+          if (hb == 0) {
+            tmem_ld_32x32b_x32(s_addr, x);
+            tmem_ld_32x32b_x32(s_addr + 32u, x + 32);
+            scales(0);
+            tmem_wait_ld();
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            uint32_t p[16];
+#pragma unroll
+            for (int v = k * kU / 2; v < (k + 1) * kU / 2; ++v) {
+              const float* xs = x + kW * v;
+              const float b = ls[v] - mw + kShift;
+              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+              const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
+#pragma unroll
+              for (int c = 0; c < kW; c += 4) {
+                float2 y0 = fma2(make_float2(xs[c], xs[c + 1]), f2, b2);
+                float2 y1 = fma2(make_float2(xs[c + 2], xs[c + 3]), f2, b2);
+                y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+                s0 = add2(s0, y0);
+                s1 = add2(s1, y1);
+                p[(kW * v + c) / 2 - 16 * k] = pack_f16x2(y0.x, y0.y);
+                p[(kW * v + c) / 2 + 1 - 16 * k] = pack_f16x2(y1.x, y1.y);
+              }
+              s0 = add2(s0, s1);
+              const float back = back0 - ls[v];
+              if (!(back > 80.f)) l = fmaf(s0.x + s0.y, ex2(back), l);
+            }
+            __syncwarp();
+            tmem_st_32x32b_x16(s_addr + 64u + 32u * hb + 16u * k, p);
+          }
+        }
+        if (lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
+        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+        tc_fence_before();
+        mbar_arrive(&bars->pfull[g]);
+      }
+      tile0 += (uint32_t)cur.tiles;
+      if (!ok) break;
+      more = next_part();
     }
     if (!ok) set_device_error(a.err, kErrWaitTimeout);
   } else {
@@ -659,37 +742,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     uint64_t* freeb = is_v ? bars->vfree : bars->kfree;
     const uint8_t* pool = is_v ? a.P.v : a.P.k;
     bool ok = true;
-    bool more = next_part();
-    int i = 0;
-    uint32_t tile = 0;
-    int tmin = 0, tmax = 0;
-    if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
-    // page of the 16 keys that this lane (u < 8) looks up, of the tile to be loaded next
-    auto lookup = [&]() -> int32_t {
-      if (!more || lane >= kSubs) return -1;
-      return sub_page(a, pt.s, tile_pos(pt.s, pt.unit0 + i, kKeys) + 16 * lane, !is_v && w == 0);
-    };
     uint4 x[kLoads];
-    auto load = [&](int32_t pg) {
-      const int pos = tile_pos(pt.s, pt.unit0 + i, kKeys);
+    bool masked = false;
+    // the codes of tile n into registers
+    auto load = [&](uint32_t n) {
+      if (!warp_wait(&bars->mfull[n % kMeta], (n / kMeta) & 1u)) return false;
+      const TileMeta& m = metas[n % kMeta];
+      const int pos = m.pos, h = m.h;
+      masked = m.whole == 0;
 #pragma unroll
       for (int it = 0; it < kLoads; ++it) {
         const int r = it * 4 * kRowsPer + r0;
-        const int32_t p = __shfl_sync(0xffffffffu, pg, r >> 4);
+        const int32_t p = m.page[r >> 4];
         x[it] = make_uint4(0u, 0u, 0u, 0u);
         if (p >= 0)
           x[it] = *reinterpret_cast<const uint4*>(
-              pool + (((size_t)p * a.Hkv + pt.s.h) * a.T.page + ((pos + r) & (a.T.page - 1))) * D + 16 * c);
+              pool + (((size_t)p * a.Hkv + h) * a.T.page + ((pos + r) & (a.T.page - 1))) * D + 16 * c);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->mfree[n % kMeta]);
+      return true;
     };
-    int32_t pg = lookup();
-    bool masked = false;
-    if (more) {
-      load(pg);
-      const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
-      masked = have != 0xFFu || !sees_all(a, tile_pos(pt.s, pt.unit0 + i, kKeys), tmin, tmax);
-    }
-    while (more) {
+    const uint32_t total = (uint32_t)run_tiles;
+    ok = load(0);
+    for (uint32_t tile = 0; tile < total && ok; ++tile) {
       if (!warp_wait(&freeb[tile & 1], ((tile >> 1) & 1u) ^ 1u)) { ok = false; break; }
       uint8_t* dst = tiles + (tile & 1) * S::kTileBytes;
       if (is_v && masked) {
@@ -732,18 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       }
       fence_proxy_async_smem();
       mbar_arrive(&full[tile & 1]);
-      ++tile;
-      if (++i == pt.tiles) {
-        i = 0;
-        more = next_part();
-        if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
-      }
-      if (more) {
-        pg = lookup();
-        load(pg);
-        const uint32_t have = __ballot_sync(0xffffffffu, pg >= 0) & 0xFFu;
-        masked = have != 0xFFu || !sees_all(a, tile_pos(pt.s, pt.unit0 + i, kKeys), tmin, tmax);
-      }
+      if (tile + 1 < total) ok = load(tile + 1);
     }
     if (!ok) set_device_error(a.err, kErrWaitTimeout);
   }
