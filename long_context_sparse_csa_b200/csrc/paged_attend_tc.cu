@@ -15,12 +15,13 @@
 // very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when a
 // tile exceeds it by more than 8 (then O is rescaled in tensor memory), so P stays below 2^15.
 //
-// Roles (640 threads): warp 0 issues the products; warp 1 looks up the tiles' pages and scales; warps 4-7 and 8-11 are the two groups' softmax, a
+// Roles (640 threads): warp 0 issues q K^T, warp 2 P V; warp 1 looks up the tiles' pages and scales; warps 4-7 and 8-11 are the two groups' softmax, a
 // thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles: 16-byte loads of codes, one tile ahead in
 // registers, to f16 in the 128-byte swizzle (two stages each).  A job is one (tile, group).  With more
 // than 128 rows (kPair) the groups take different rows of the same tile; otherwise the same rows of
-// alternate tiles, joined by the combine kernel.  Order of the products: QK(j), PV(j - 1); QK of a group
-// overwrites the P that its last PV read, so it waits for that product to complete.
+// alternate tiles, joined at the end.  A group works through half tiles in two buffers of S: while it
+// weighs one, the other's scores are computed.  P lies over its S, so the next S there waits for the product
+// that reads it.
 #include <cuda_fp16.h>
 
 #include "paged_walk.cuh"
@@ -42,16 +43,18 @@ static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= kThr
 
 struct __align__(8) TcBars {
   uint64_t kfull[2], kfree[2], vfull[2], vfree[2];
-  uint64_t qfull[2], sfull[2], pfull[2], pvdone[2], ofree[2];
+  uint64_t qfull[2], ofree[2];
+  uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];      // [group][S buffer]
   uint64_t recfull, recfree;
   uint64_t mfull[kMeta], mfree[kMeta];
   uint32_t tmem_base;
 };
 
 // What the other roles need of a key tile, looked up ahead by one warp.
-struct TileMeta {
+struct __align__(16) TileMeta {
   int32_t page[kSubs];                        // page of each 16 keys, -1: none
   float ks[kSubs], lv[kSubs];                 // key scale, log2 of the value scale
+  float lv_min[2];                            // the smallest lv of each half
   int pos, h;                                 // first position, KV head
   int index;                                  // number of the tile in its part
   int whole;                                  // every row of the block sees every key
@@ -88,7 +91,7 @@ struct TcShape {
   static constexpr size_t kOffNan = kOffCq + 2 * 128 * 4;     // [2 stages][32] NaN flags of V's rows, four to a byte
   static constexpr size_t kOffBars = kOffNan + 64;
   static constexpr size_t kOffScan = kOffBars + (sizeof(TcBars) + 7) / 8 * 8;
-  static constexpr size_t kOffMeta = kOffScan + (kThreads / 32) * 8;
+  static constexpr size_t kOffMeta = (kOffScan + (kThreads / 32) * 8 + 15) / 16 * 16;
   static constexpr size_t kOffWalk = kOffMeta + kMeta * sizeof(TileMeta);
   static constexpr size_t kBytes = 1024 + kOffWalk + (kThreads / 32) * sizeof(WarpWalk);
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -183,8 +186,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// A whole warp's wait: true for all its lanes or for none.
+// A whole warp's bounded wait: true for all its lanes or for none.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;
   return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 
@@ -248,16 +252,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       mbar_init(&bars->vfull[i], 128);
       mbar_init(&bars->vfree[i], 1);
       mbar_init(&bars->qfull[i], 128);
-      mbar_init(&bars->sfull[i], 1);
-      mbar_init(&bars->pfull[i], 128);
-      mbar_init(&bars->pvdone[i], 1);
+      for (int u = 0; u < 2; ++u) {
+        mbar_init(&bars->sfull[i][u], 1);
+        mbar_init(&bars->pfull[i][u], 128);
+        mbar_init(&bars->pvdone[i][u], 1);
+      }
       mbar_init(&bars->ofree[i], 128);
     }
     mbar_init(&bars->recfull, 128);
     mbar_init(&bars->recfree, 128);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(&bars->mfull[i], kSubs);
-      mbar_init(&bars->mfree[i], 9 + (kPair ? 8 : 4));   // a lane of every warp that reads the entry
+      mbar_init(&bars->mfree[i], 10 + (kPair ? 8 : 4));   // a lane of every warp that reads the entry
     }
     fence_barrier_init();
   }
@@ -287,111 +293,105 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     // ------------------------------------------------------------------ the products
     regs_dec<kRegsIssue>();
     if (warp == 0) {
-      const uint32_t idesc_s = instr_desc(128, kKeys, 0u);
-      const uint32_t idesc_o = instr_desc(128, D, 0u) | (1u << 16);          // V: dims-major
+      // S = q K^T, a half tile at a time into the group's two buffers in turns
+      const uint32_t idesc = instr_desc(128, 64, 0u), lead = elect_lane();
       const uint64_t q_desc = desc_kmajor_sw128(smem_u32(sm));
       const uint64_t k_desc = desc_kmajor_sw128(smem_u32(sm + S::kOffK));
-      const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(sm + S::kOffV), S::kHalf, 1024u);
-      const uint32_t lead = elect_lane();
       bool ok = true;
-      uint32_t jpar[2] = {0, 0}, qpar[2] = {0, 0}, opar[2] = {0, 0};         // parities of a group's jobs, queries, O
-      bool begun[2] = {false, false};
-      // S of group g from K stage st
-      auto qk = [&](int g, uint32_t st, bool first, bool last_use) {
+      uint32_t cnt[2] = {0, 0}, qpar[2] = {0, 0};            // the groups' jobs so far, parity of their queries
+      auto qk = [&](int g, int half, uint32_t st, bool first) {
         if (first) {
           ok = ok && warp_wait(&bars->qfull[g], qpar[g]);
           qpar[g] ^= 1u;
         }
-        // the group's last P has been read (its columns are S's)
-        if (begun[g]) ok = ok && warp_wait(&bars->pvdone[g], jpar[g] ^ 1u);
+        // the buffer's last P has been read
+        const uint32_t buf = cnt[g] & 1u;
+        ok = ok && warp_wait(&bars->pvdone[g][buf], ((cnt[g] >> 1) & 1u) ^ 1u);
         if (!ok) return;
-        begun[g] = true;
-        jpar[g] ^= 1u;
+        ++cnt[g];
         tc_fence_after();
         const uint64_t qd = q_desc + (uint64_t)(g * (S::kTileBytes >> 4));
-        const uint64_t kd = k_desc + (uint64_t)(st * (S::kTileBytes >> 4));
+        const uint64_t kd = k_desc + (uint64_t)(st * (S::kTileBytes >> 4) + half * 512u);
 #pragma unroll
         for (int h = 0; h < kHalves; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            umma_ss(lead, tmem + g * 128u, qd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk),
-                    kd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk), idesc_s, (h | kk) ? 1u : 0u);
-        commit_if(lead, &bars->sfull[g]);
-        if (last_use) commit_if(lead, &bars->kfree[st]);
-      };
-      // O of group g from V stage st (of tile n)
-      auto pv = [&](int g, uint32_t n, bool first, bool last_use) {
-        const uint32_t st = n & 1u;
-        ok = ok && warp_wait(&bars->vfull[st], (n >> 1) & 1u);
-        if (first) {                                       // O of the group's last part has been read
-          ok = ok && warp_wait(&bars->ofree[g], opar[g] ^ 1u);
-          opar[g] ^= 1u;
-        }
-        ok = ok && warp_wait(&bars->pfull[g], jpar[g] ^ 1u);
-        if (!ok) return;
-        tc_fence_after();
-        const uint64_t vd = v_desc + (uint64_t)(st * (S::kTileBytes >> 4));
-        const uint32_t od = tmem + 256u + (uint32_t)(g * D), pd = tmem + g * 128u + 64u;
-#pragma unroll
-        for (int kk = 0; kk < kKeys / 16; ++kk)
-          umma_ts(lead, od, pd + 8u * kk, vd + (uint64_t)((kk * 2048) >> 4), idesc_o, (first && kk == 0) ? 0u : 1u);
-        commit_if(lead, &bars->pvdone[g]);
-        if (last_use) commit_if(lead, &bars->vfree[st]);
-      };
-      // K tile n has landed; its number in its part (the conversion has seen the entry: K waits for it)
-      auto arrival = [&](uint32_t n) {
-        ok = ok && warp_wait(&bars->kfull[n & 1u], (n >> 1) & 1u);
-        const int idx = metas[n % kMeta].index;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->mfree[n % kMeta]);
-        return idx;
+            umma_ss(lead, tmem + g * 128u + 64u * buf, qd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk),
+                    kd + (uint64_t)(h * (S::kHalf >> 4) + 2 * kk), idesc, (h | kk) ? 1u : 0u);
+        commit_if(lead, &bars->sfull[g][buf]);
       };
       const uint32_t total = (uint32_t)run_tiles;
-      if (kPair) {
-        // QK0(n), PV1(n - 1), QK1(n), PV0(n)
-        bool first = false;
 #pragma unroll 1
-        for (uint32_t n = 0; n < total && ok; ++n) {
-          const bool before = first;
-          first = arrival(n) == 0;
-          qk(0, n & 1u, first, false);
-          if (n > 0) pv(1, n - 1, before, true);
-          qk(1, n & 1u, first, true);
-          pv(0, n, first, false);
-        }
-        pv(1, total - 1, first, true);
-      } else {
-        // QK(n), PV(n - 1), the groups in turns; after a part of an odd number of tiles the same group
-        // comes twice, and its PV first
-        int g = 0;
-        bool first = false;
+      for (uint32_t n = 0; n < total && ok; ++n) {
+        ok = warp_wait(&bars->kfull[n & 1u], (n >> 1) & 1u);
+        if (!ok) break;
+        const int idx = metas[n % kMeta].index;              // the conversion has seen the entry
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->mfree[n % kMeta]);
 #pragma unroll 1
-        for (uint32_t n = 0; n < total && ok; ++n) {
-          const int pg = g;
-          const bool before = first;
-          const int idx = arrival(n);
-          g = idx & 1;
-          first = idx < 2;
-          const bool early = n > 0 && pg == g;
-          if (early) {
-            if (g) pv(1, n - 1, before, true);
-            else pv(0, n - 1, before, true);
-          }
-          if (g) {
-            qk(1, n & 1u, first, true);
-            if (n > 0 && !early) pv(0, n - 1, before, true);
+        for (int half = 0; half < 2; ++half) {
+          if (kPair) {
+            qk(0, half, n & 1u, idx + half == 0);
+            qk(1, half, n & 1u, idx + half == 0);
+          } else if (idx & 1) {
+            qk(1, half, n & 1u, idx < 2 && half == 0);
           } else {
-            qk(0, n & 1u, first, true);
-            if (n > 0 && !early) pv(1, n - 1, before, true);
+            qk(0, half, n & 1u, idx < 2 && half == 0);
           }
         }
-        if (g) pv(1, total - 1, first, true);
-        else pv(0, total - 1, first, true);
+        commit_if(lead, &bars->kfree[n & 1u]);
       }
       if (!ok) set_device_error(a.err, kErrWaitTimeout);
       // nothing of this warp is in flight when tensor memory is released
-      if (begun[0]) warp_wait(&bars->pvdone[0], jpar[0] ^ 1u);
-      if (begun[1]) warp_wait(&bars->pvdone[1], jpar[1] ^ 1u);
+      for (int g = 0; g < 2; ++g)
+        if (cnt[g] > 0) warp_wait(&bars->sfull[g][(cnt[g] - 1) & 1u], ((cnt[g] - 1) >> 1) & 1u);
+    } else if (warp == 2) {
+      // O += P V
+      const uint32_t idesc = instr_desc(128, D, 0u) | (1u << 16), lead = elect_lane();        // V: dims-major
+      const uint64_t v_desc = desc_mnmajor_sw128(smem_u32(sm + S::kOffV), S::kHalf, 1024u);
+      bool ok = true;
+      uint32_t cnt[2] = {0, 0}, opar[2] = {0, 0};
+      auto pv = [&](int g, int half, uint32_t st, bool first) {
+        if (first) {                                         // O of the group's last part has been read
+          ok = ok && warp_wait(&bars->ofree[g], opar[g] ^ 1u);
+          opar[g] ^= 1u;
+        }
+        const uint32_t buf = cnt[g] & 1u;
+        ok = ok && warp_wait(&bars->pfull[g][buf], (cnt[g] >> 1) & 1u);
+        if (!ok) return;
+        ++cnt[g];
+        tc_fence_after();
+        const uint64_t vd = v_desc + (uint64_t)(st * (S::kTileBytes >> 4) + half * 512u);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          umma_ts(lead, tmem + 256u + (uint32_t)(g * D), tmem + g * 128u + 64u * buf + 8u * kk,
+                  vd + (uint64_t)((kk * 2048) >> 4), idesc, (first && kk == 0) ? 0u : 1u);
+        commit_if(lead, &bars->pvdone[g][buf]);
+      };
+      const uint32_t total = (uint32_t)run_tiles;
+#pragma unroll 1
+      for (uint32_t n = 0; n < total && ok; ++n) {
+        ok = warp_wait(&bars->vfull[n & 1u], (n >> 1) & 1u);
+        if (!ok) break;
+        const int idx = metas[n % kMeta].index;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->mfree[n % kMeta]);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (kPair) {
+            pv(0, half, n & 1u, idx + half == 0);
+            pv(1, half, n & 1u, idx + half == 0);
+          } else if (idx & 1) {
+            pv(1, half, n & 1u, idx < 2 && half == 0);
+          } else {
+            pv(0, half, n & 1u, idx < 2 && half == 0);
+          }
+        }
+        commit_if(lead, &bars->vfree[n & 1u]);
+      }
+      if (!ok) set_device_error(a.err, kErrWaitTimeout);
+      for (int g = 0; g < 2; ++g)
+        if (cnt[g] > 0) warp_wait(&bars->pvdone[g][(cnt[g] - 1) & 1u], ((cnt[g] - 1) >> 1) & 1u);
     } else if (warp == 1) {
       // ---------------------------------------------------------------- pages and scales, four tiles at a time
       bool ok = true;
@@ -434,6 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           vs = a.P.vs[gh];
         }
         const uint32_t have = (__ballot_sync(0xffffffffu, pg >= 0) >> (lane & 24)) & 0xFFu;
+        const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 255u) - 127);
+        float lm = fminf(lv, __shfl_xor_sync(0xffffffffu, lv, 1));
+        lm = fminf(lm, __shfl_xor_sync(0xffffffffu, lm, 2));
         const int e = (int)((n0 + (lane >> 3)) & (kMeta - 1));
         bool w = true;
         if (mine) w = mbar_wait(&bars->mfree[e], (uint32_t)(((n0 + (lane >> 3)) / kMeta) & 1) ^ 1u);
@@ -442,7 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           TileMeta& m = metas[e];
           m.page[u] = pg;
           m.ks[u] = ks;
-          m.lv[u] = (float)((int)((__float_as_uint(vs) >> 23) & 255u) - 127);
+          m.lv[u] = lv;
+          if ((u & 3) == 0) m.lv_min[u >> 2] = lm;
           if (u == 0) {
             m.pos = pos;
             m.h = h;
@@ -465,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const uint32_t s_addr = lane_addr + (uint32_t)(g * 128), o_addr = lane_addr + 256u + (uint32_t)(g * D);
     uint8_t* Q = sm + (size_t)g * S::kTileBytes;
     bool ok = true;
-    uint32_t job = 0, tile0 = 0, shared = 0;            // jobs of this group, tiles of the CTA, segments shared by the groups
+    uint32_t job = 0, tile0 = 0, shared = 0;            // half tiles of this group, tiles of the CTA, segments shared by the groups
 
     // The group's queries: D / 8 lanes a row, scaled by a power of two to at most 2^15, as f16.
     auto load_q = [&](const Part& p) {
@@ -508,6 +512,32 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       mbar_arrive(&bars->qfull[g]);
     };
 
+    // Scores of a half tile that the row at position t does not see become -inf, in tensor memory, and NaN
+    // where the key's V row has a NaN code.  16 columns at a time: the loops stay small (see the top).
+    auto hide = [&](const TileMeta& meta, int half, uint32_t tile, uint32_t sb, int t) {
+#pragma unroll 1
+      for (int u = 0; u < 4; ++u) {
+        float y[16];
+        uint32_t yw[16];
+        __syncwarp();
+        tmem_ld_32x32b_x16(sb + 16u * u, y);
+        tmem_wait_ld();
+        const int su = 4 * half + u, p0 = meta.pos + 16 * su;
+        uint32_t m = bits_to(t - p0);
+        if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
+        if (t < 0 || !((meta.have >> su) & 1u)) m = 0u;
+        const uint32_t nb = *reinterpret_cast<const uint32_t*>(nans + (tile & 1) * 32 + 4 * su);
+        const uint32_t bad = ((nb & 15u) | ((nb >> 4) & 0xF0u) | ((nb >> 8) & 0xF00u) | ((nb >> 12) & 0xF000u)) & m;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const float v = (m >> c) & 1u ? y[c] : -INFINITY;
+          yw[c] = (bad >> c) & 1u ? 0x7fffffffu : __float_as_uint(v);
+        }
+        tmem_st_32x32b_x16(sb + 16u * u, yw);
+      }
+      tmem_wait_st();
+    };
+
     // Per part: its tiles; then the next part's queries, while the last product runs; then its end.
     Part& cur = walk.cur;
     float mw = kNone, mz = kNone, l = 0.f, cq = 0.f;
@@ -534,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       const int rr = (kPair ? g * 128 : 0) + row;
       const bool live = j < cur.s.n;
       const int head = cur.s.h * a.G + gr;
-      if (jobs > 0 && !warp_wait(&bars->pvdone[g], (job - 1) & 1u)) return false;
+      if (jobs > 0 && !warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u)) return false;
       tc_fence_after();
       const float* other = rec + record_floats(kRowTile, D);                 // group 1's record, for group 0
       // the record of the last shared segment has been read
@@ -627,66 +657,30 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       gr = R - j * a.G;
       t = j < cur.s.n ? cur.s.start + j : -1;
       cq = cqs[g * 128 + row];
-      for (int i = 0; i < jobs && ok; ++i, ++job) {
+      for (int i = 0; i < jobs && ok; ++i) {
         const uint32_t tile = tile0 + (uint32_t)(kPair ? i : 2 * i + g);
         if (!warp_wait(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { ok = false; break; }
         const TileMeta& meta = metas[tile % kMeta];
-        const int pos = meta.pos;
         const bool whole = meta.whole != 0;
-        if (!warp_wait(&bars->sfull[g], job & 1u)) { ok = false; break; }
-        if (!whole && !warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u)) { ok = false; break; }   // the NaN flags
-        tc_fence_after();
-        if (!whole) {
-          // scores that the row does not see become -inf, and NaN where the key's V row has a NaN code
+        if (__builtin_expect(!whole, 0) && !warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u)) { ok = false; break; }   // the NaN flags
 #pragma unroll 1
-          for (int q = 0; q < 4; ++q) {
-            float y[32];
-            __syncwarp();
-            tmem_ld_32x32b_x32(s_addr + 32u * q, y);
-            tmem_wait_ld();
-            const int p0 = pos + 32 * q;
-            uint32_t m = bits_to(t - p0);
-            if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
-            const uint32_t hv = (meta.have >> (2 * q)) & 3u;
-            m &= ((hv & 1u) ? 0xFFFFu : 0u) | ((hv & 2u) ? 0xFFFF0000u : 0u);
-            if (t < 0) m = 0u;
-            const uint2 nb = *reinterpret_cast<const uint2*>(nans + (tile & 1) * 32 + 8 * q);
-            uint32_t nan32 = 0;
-#pragma unroll
-            for (int c = 0; c < 4; ++c)
-              nan32 |= ((nb.x >> (8 * c)) & 15u) << (4 * c) | ((nb.y >> (8 * c)) & 15u) << (16 + 4 * c);
-            nan32 &= m;
-#pragma unroll
-            for (int c = 0; c < 32; ++c) {
-              if (!((m >> c) & 1u)) y[c] = -INFINITY;
-              if ((nan32 >> c) & 1u) y[c] = __int_as_float(0x7fffffff);
-            }
-            tmem_st_32x32b_x32(s_addr + 32u * q, y);
-          }
-          tmem_wait_st();
-        }
-        // Half of the tile's scores (64 columns) in registers at a time: the maxima of the first half, then of
-        // the second; P of the second while it is there; the first half read once more.  P takes columns
-        // [64, 128) of S, so that what is written has always been read.  The loops stay rolled: unrolled, the
-        // roles' code does not fit the instruction caches (2,050 us instead of the present time for the chunk
-        // of 2,048 tokens behind 14,336).
-        constexpr int kU = 64 / kW;                      // scales in a half
-        float x[64], fs[kU], ls[kU];                     // logit factor and log2 of the value scale per kW columns
-        auto scales = [&](int hb) {
+        for (int half = 0; half < 2; ++half, ++job) {
+          const uint32_t buf = job & 1u, sb = s_addr + 64u * buf;
+          if (!warp_wait(&bars->sfull[g][buf], (job >> 1) & 1u)) { ok = false; break; }
+          tc_fence_after();
+          constexpr int kU = 64 / kW;                    // scales in a half
+          float x[64], fs[kU], ls[kU];                   // scores; logit factor, log2 of the value scale per kW columns
+          if (__builtin_expect(!whole, 0)) hide(meta, half, tile, sb, t);
+          tmem_ld_32x32b_x32(sb, x);
+          tmem_ld_32x32b_x32(sb + 32u, x + 32);
 #pragma unroll
           for (int v = 0; v < kU; ++v) {
-            const int u = 4 * hb + v * (kW / 16);
+            const int u = 4 * half + v * (kW / 16);
             fs[v] = fmaxf(fminf(meta.ks[u] * cq, 3.0e38f), 1.2e-38f);
             ls[v] = meta.lv[u];
           }
-        };
-        float cz = -INFINITY, cw = -INFINITY;
-#pragma unroll 1
-        for (int hb = 0; hb < 2; ++hb) {
-          tmem_ld_32x32b_x32(s_addr + 64u * hb, x);
-          tmem_ld_32x32b_x32(s_addr + 64u * hb + 32u, x + 32);
-          scales(hb);
           tmem_wait_ld();
+          float cz = -INFINITY, cw = -INFINITY;
 #pragma unroll
           for (int v = 0; v < kU; ++v) {
             float t0 = fmaxf(x[kW * v], x[kW * v + 1]), t1 = fmaxf(x[kW * v + 2], x[kW * v + 3]);
@@ -699,54 +693,44 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             cz = fmaxf(cz, zt);
             cw = fmaxf(cw, zt + ls[v]);
           }
-        }
-        const bool move = cw > mw + kMargin || cz > mz + 40.f;
-        if (__any_sync(0xffffffffu, move)) {
-          const float nw = move ? fmaxf(mw, cw) : mw, nz = move ? fmaxf(mz, cz) : mz;
-          const float al = ex2(mw - nw);
-          l *= ex2(mz - nz);
-          mw = nw;
-          mz = nz;
-          if (i > 0) {
+          const bool move = cw > mw + kMargin || cz > mz + 40.f;
+          if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
+            const float nw = move ? fmaxf(mw, cw) : mw, nz = move ? fmaxf(mz, cz) : mz;
+            const float al = ex2(mw - nw);
+            l *= ex2(mz - nz);
+            mw = nw;
+            mz = nz;
+            if (i + half > 0) {                          // O, once the group's last product is complete
+              if (!warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u)) { ok = false; break; }
+              tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
-              float o[16];
-              tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
+              for (int c = 0; c < D; c += 16) {
+                float o[16];
+                tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
+                tmem_wait_ld();
+                uint32_t ow[16];
+#pragma unroll
+                for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
+                tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
+              }
+            }
+          }
+          // denominators whose factor is out of range: their exponentials apart
+          const float back0 = mw - mz - kShift;
+          if (__builtin_expect(__any_sync(0xffffffffu, back0 - meta.lv_min[half] > 80.f), 0)) {
+#pragma unroll 1
+            for (int u = 0; u < 4; ++u) {
+              float y[16];
+              __syncwarp();
+              tmem_ld_32x32b_x16(sb + 16u * u, y);
               tmem_wait_ld();
-              uint32_t ow[16];
+              const float fq = fmaxf(fminf(meta.ks[4 * half + u] * cq, 3.0e38f), 1.2e-38f);
+              if (back0 - meta.lv[4 * half + u] > 80.f) {
 #pragma unroll
-              for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
-              tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
+                for (int c = 0; c < 16; ++c) l += ex2(y[c] * fq - mz);
+              }
             }
-          }
-        }
-        // denominators whose factor is out of range: their exponentials apart
-        const float back0 = mw - mz - kShift;
-        bool far = false;
-#pragma unroll
-        for (int u = 0; u < kSubs; ++u) far |= back0 - meta.lv[u] > 80.f;
-        if (__any_sync(0xffffffffu, far)) {
-#pragma unroll 1
-          for (int q = 0; q < 8; ++q) {
-            float y[16];
             __syncwarp();
-            tmem_ld_32x32b_x16(s_addr + 16u * q, y);
-            tmem_wait_ld();
-            const float fq = fmaxf(fminf(meta.ks[q] * cq, 3.0e38f), 1.2e-38f);
-            if (back0 - meta.lv[q] > 80.f) {
-#pragma unroll
-              for (int c = 0; c < 16; ++c) l += ex2(y[c] * fq - mz);
-            }
-          }
-          __syncwarp();
-        }
-#pragma unroll 1
-        for (int hb = 1; hb >= 0; --hb) {
-          if (hb == 0) {
-            tmem_ld_32x32b_x32(s_addr, x);
-            tmem_ld_32x32b_x32(s_addr + 32u, x + 32);
-            scales(0);
-            tmem_wait_ld();
           }
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -772,13 +756,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               if (!(back > 80.f)) l = fmaf(s0.x + s0.y, ex2(back), l);
             }
             __syncwarp();
-            tmem_st_32x32b_x16(s_addr + 64u + 32u * hb + 16u * k, p);
+            tmem_st_32x32b_x16(sb + 16u * k, p);
           }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->pfull[g][buf]);
         }
         if (lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
-        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-        tc_fence_before();
-        mbar_arrive(&bars->pfull[g]);
       }
       tile0 += (uint32_t)cur.tiles;
       if (!ok) break;
@@ -800,20 +784,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     bool ok = true;
     uint4 x[kLoads];
     bool masked = false;
+    uint32_t have = 0;
     // the codes of tile n into registers
     auto load = [&](uint32_t n) {
       if (!warp_wait(&bars->mfull[n % kMeta], (n / kMeta) & 1u)) return false;
       const TileMeta& m = metas[n % kMeta];
-      const int pos = m.pos, h = m.h;
       masked = m.whole == 0;
+      have = m.have;
+      int32_t pg[kSubs];
+      *reinterpret_cast<int4*>(pg) = *reinterpret_cast<const int4*>(m.page);
+      *reinterpret_cast<int4*>(pg + 4) = *reinterpret_cast<const int4*>(m.page + 4);
+      const uint8_t* base = pool + (size_t)m.h * a.T.page * D + 16 * c;
+      const int at = m.pos + r0, inside = a.T.page - 1;
+      const size_t per = (size_t)a.Hkv * a.T.page * D;
 #pragma unroll
       for (int it = 0; it < kLoads; ++it) {
-        const int r = it * 4 * kRowsPer + r0;
-        const int32_t p = m.page[r >> 4];
-        x[it] = make_uint4(0u, 0u, 0u, 0u);
-        if (p >= 0)
-          x[it] = *reinterpret_cast<const uint4*>(
-              pool + (((size_t)p * a.Hkv + h) * a.T.page + ((pos + r) & (a.T.page - 1))) * D + 16 * c);
+        // rows without a page read page 0 (and are cleared below)
+        const int r = it * 4 * kRowsPer;
+        const int32_t p0 = pg[r >> 4], p1 = pg[(r >> 4) + (kRowsPer == 8 ? 1 : 0)];
+        const int32_t p = kRowsPer == 8 && w >= 2 ? p1 : p0;
+        x[it] = *reinterpret_cast<const uint4*>(base + (size_t)(p < 0 ? 0 : p) * per + (size_t)((at + r) & inside) * D);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->mfree[n % kMeta]);
@@ -830,6 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         for (int it = 0; it < kLoads; ++it) {
           uint32_t* xw = reinterpret_cast<uint32_t*>(&x[it]);
           uint32_t any = 0;
+          if (!((have >> ((it * 4 * kRowsPer + r0) >> 4)) & 1u)) x[it] = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t nb = nan_bytes(xw[q]);
