@@ -12,8 +12,8 @@
 // the warp-level kernel: O sums 2^(z + v - mw + 7) codes, z the logit in log2 units and v the log2 of the
 // page's value scale; the denominator sums 2^(z - mz).  One exponential serves both: per 16 keys of a
 // page the weights' sum times 2^(mw - mz - v - 7), unless that factor is beyond 2^80 (pages' scales
-// very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when a
-// tile exceeds it by more than 8 (then O is rescaled in tensor memory), so P stays below 2^15.
+// very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when
+// some keys exceed it by more than 8 (then O is rescaled in tensor memory), so P stays up to 2^15.
 //
 // Roles (640 threads): warp 0 issues q K^T, warp 2 P V; warp 1 looks up the tiles' pages and scales; warps 4-7 and 8-11 are the two groups' softmax, a
 // thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles: 16-byte loads of codes, one tile ahead in
@@ -37,7 +37,7 @@ constexpr int kKeys = 128;
 constexpr int kThreads = 640;
 constexpr int kSubs = kKeys / 16;
 constexpr int kMeta = 8;                        // tiles looked up ahead, four at a time
-constexpr float kShift = 7.f, kMargin = 8.f;
+constexpr float kShift = 7.f;
 constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsConvert = 72, kRegsIssue = 80;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
 
@@ -668,96 +668,129 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           const uint32_t buf = job & 1u, sb = s_addr + 64u * buf;
           if (!warp_wait(&bars->sfull[g][buf], (job >> 1) & 1u)) { ok = false; break; }
           tc_fence_after();
-          constexpr int kU = 64 / kW;                    // scales in a half
-          float x[64], fs[kU], ls[kU];                   // scores; logit factor, log2 of the value scale per kW columns
           if (__builtin_expect(!whole, 0)) hide(meta, half, tile, sb, t);
-          tmem_ld_32x32b_x32(sb, x);
-          tmem_ld_32x32b_x32(sb + 32u, x + 32);
-#pragma unroll
-          for (int v = 0; v < kU; ++v) {
-            const int u = 4 * half + v * (kW / 16);
-            fs[v] = fmaxf(fminf(meta.ks[u] * cq, 3.0e38f), 1.2e-38f);
-            ls[v] = meta.lv[u];
-          }
-          tmem_wait_ld();
-          float cz = -INFINITY, cw = -INFINITY;
-#pragma unroll
-          for (int v = 0; v < kU; ++v) {
-            float t0 = fmaxf(x[kW * v], x[kW * v + 1]), t1 = fmaxf(x[kW * v + 2], x[kW * v + 3]);
-#pragma unroll
-            for (int c = 4; c < kW; c += 4) {
-              t0 = fmaxf(t0, fmaxf(x[kW * v + c], x[kW * v + c + 1]));
-              t1 = fmaxf(t1, fmaxf(x[kW * v + c + 2], x[kW * v + c + 3]));
-            }
-            const float zt = fmaxf(t0, t1) * fs[v];
-            cz = fmaxf(cz, zt);
-            cw = fmaxf(cw, zt + ls[v]);
-          }
-          const bool move = cw > mw + kMargin || cz > mz + 40.f;
-          if (__builtin_expect(__any_sync(0xffffffffu, move), 0)) {
-            const float nw = move ? fmaxf(mw, cw) : mw, nz = move ? fmaxf(mz, cz) : mz;
-            const float al = ex2(mw - nw);
-            l *= ex2(mz - nz);
-            mw = nw;
-            mz = nz;
-            if (i + half > 0) {                          // O, once the group's last product is complete
-              if (!warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u)) { ok = false; break; }
-              tc_fence_after();
+          // 32 keys at a time: P against the present maxima; where that leaves P's range (above 2^15: a part's first
+          // keys, a new maximum), the maxima move and P is formed once more.  So the maxima are taken of P, in pairs,
+          // beside the exponentials, not of the scores before them.  The loops stay rolled and short: with the
+          // half tile unrolled the roles' code does not fit the innermost instruction cache.
+          constexpr int kU = 32 / kW;                    // scales in 32 keys
 #pragma unroll 1
-              for (int c = 0; c < D; c += 16) {
-                float o[16];
-                tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
-                tmem_wait_ld();
-                uint32_t ow[16];
-#pragma unroll
-                for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
-                tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
-              }
-            }
-          }
-          // denominators whose factor is out of range: their exponentials apart
-          const float back0 = mw - mz - kShift;
-          if (__builtin_expect(__any_sync(0xffffffffu, back0 - meta.lv_min[half] > 80.f), 0)) {
-#pragma unroll 1
-            for (int u = 0; u < 4; ++u) {
-              float y[16];
-              __syncwarp();
-              tmem_ld_32x32b_x16(sb + 16u * u, y);
-              tmem_wait_ld();
-              const float fq = fmaxf(fminf(meta.ks[4 * half + u] * cq, 3.0e38f), 1.2e-38f);
-              if (back0 - meta.lv[4 * half + u] > 80.f) {
-#pragma unroll
-                for (int c = 0; c < 16; ++c) l += ex2(y[c] * fq - mz);
-              }
-            }
-            __syncwarp();
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 2 && ok; ++k) {
+            const int u0 = 4 * half + 2 * k;
+            float ls[kU], sums[kU];                      // log2 of the value scale, weights' sum per kW columns
             uint32_t p[16];
+            bool far = false;
+#pragma unroll 1
+            for (int again = 0;; ++again) {
+              float x[32], fs[kU];
+              __syncwarp();
+              tmem_ld_32x32b_x32(sb + 32u * k, x);
 #pragma unroll
-            for (int v = k * kU / 2; v < (k + 1) * kU / 2; ++v) {
-              const float* xs = x + kW * v;
-              const float b = ls[v] - mw + kShift;
-              float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-              const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
-#pragma unroll
-              for (int c = 0; c < kW; c += 4) {
-                float2 y0 = fma2(make_float2(xs[c], xs[c + 1]), f2, b2);
-                float2 y1 = fma2(make_float2(xs[c + 2], xs[c + 3]), f2, b2);
-                y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
-                s0 = add2(s0, y0);
-                s1 = add2(s1, y1);
-                p[(kW * v + c) / 2 - 16 * k] = pack_f16x2(y0.x, y0.y);
-                p[(kW * v + c) / 2 + 1 - 16 * k] = pack_f16x2(y1.x, y1.y);
+              for (int v = 0; v < kU; ++v) {
+                fs[v] = fmaxf(fminf(meta.ks[u0 + v] * cq, 3.0e38f), 1.2e-38f);
+                ls[v] = meta.lv[u0 + v];
               }
-              s0 = add2(s0, s1);
+              const float lv_min = meta.lv_min[half];
+              tmem_wait_ld();
+              __half2 top = __float2half2_rn(0.f);
+#pragma unroll
+              for (int v = 0; v < kU; ++v) {
+                const float* xs = x + kW * v;
+                const float b = ls[v] - mw + kShift;
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
+#pragma unroll
+                for (int c = 0; c < kW; c += 4) {
+                  float2 y0 = fma2(make_float2(xs[c], xs[c + 1]), f2, b2);
+                  float2 y1 = fma2(make_float2(xs[c + 2], xs[c + 3]), f2, b2);
+                  y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+                  s0 = add2(s0, y0);
+                  s1 = add2(s1, y1);
+                  const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
+                  top = __hmax2(top, __hmax2(h0, h1));
+                  p[(kW * v + c) / 2] = *reinterpret_cast<const uint32_t*>(&h0);
+                  p[(kW * v + c) / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
+                }
+                s0 = add2(s0, s1);
+                sums[v] = s0.x + s0.y;
+              }
+              if (again) break;
+              const bool over = fmaxf(__low2float(top), __high2float(top)) > 32768.f;
+              far = mw - mz - kShift - lv_min > 80.f;
+              if (__builtin_expect(!__any_sync(0xffffffffu, over || far), 1)) break;
+              far = true;
+              if (!__any_sync(0xffffffffu, over)) break;
+              float cz = -INFINITY, cw = -INFINITY;
+#pragma unroll 1
+              for (int u = 0; u < 2; ++u) {
+                float y[16];
+                tmem_ld_32x32b_x16(sb + 32u * k + 16u * u, y);
+                tmem_wait_ld();
+                float m16 = y[0];
+#pragma unroll
+                for (int c = 1; c < 16; ++c) m16 = fmaxf(m16, y[c]);
+                const float zt = m16 * fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
+                cz = fmaxf(cz, zt);
+                cw = fmaxf(cw, zt + meta.lv[u0 + u]);
+              }
+              const float nw = over ? fmaxf(mw, cw) : mw, nz = over ? fmaxf(mz, cz) : mz;
+              const float al = ex2(mw - nw);
+              l *= ex2(mz - nz);
+              mw = nw;
+              mz = nz;
+              if (k > 0) {                               // the half tile's first P
+                float y[16];
+                uint32_t yw[16];
+                tmem_ld_32x32b_x16(sb, y);
+                tmem_wait_ld();
+                const __half2 a2 = __float2half2_rn(al);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) {
+                  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[q]), a2);
+                  yw[q] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                tmem_st_32x32b_x16(sb, yw);
+              }
+              if (i + half > 0) {                        // O, once the group's last product is complete
+                if (!warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u)) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 16) {
+                  float o[16];
+                  tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
+                  tmem_wait_ld();
+                  uint32_t ow[16];
+#pragma unroll
+                  for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
+                  tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
+                }
+              }
+            }
+            const float back0 = mw - mz - kShift;
+            if (__builtin_expect(far, 0)) {
+              // denominators whose factor is out of range: their exponentials apart
+#pragma unroll 1
+              for (int u = 0; u < 2; ++u) {
+                float y[16];
+                __syncwarp();
+                tmem_ld_32x32b_x16(sb + 32u * k + 16u * u, y);
+                tmem_wait_ld();
+                const float fq = fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
+                if (back0 - meta.lv[u0 + u] > 80.f) {
+#pragma unroll
+                  for (int c = 0; c < 16; ++c) l += ex2(y[c] * fq - mz);
+                }
+              }
+            }
+#pragma unroll
+            for (int v = 0; v < kU; ++v) {
               const float back = back0 - ls[v];
-              if (!(back > 80.f)) l = fmaf(s0.x + s0.y, ex2(back), l);
+              if (!(back > 80.f)) l = fmaf(sums[v], ex2(back), l);
             }
             __syncwarp();
-            tmem_st_32x32b_x16(sb + 16u * k, p);
+            tmem_st_32x32b_x16(sb + 16u * k, p);         // over columns of S that have been read
           }
+          if (!ok) break;
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars->pfull[g][buf]);
@@ -838,20 +871,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           }
         }
       }
+#pragma unroll 1
+      for (int i0 = 0; i0 < kLoads; i0 += kLoads / 2) {
 #pragma unroll
-      for (int it = 0; it < kLoads; ++it) {
-        const int r = it * 4 * kRowsPer + r0;
-        const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
-        uint4 y0, y1;
-        e4m3x4_f16(xw[0], y0.x, y0.y);
-        e4m3x4_f16(xw[1], y0.z, y0.w);
-        e4m3x4_f16(xw[2], y1.x, y1.y);
-        e4m3x4_f16(xw[3], y1.z, y1.w);
-        // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
-        uint8_t* at = dst + (c >> 2) * S::kHalf;
-        const int jx = (c & 3) * 2, up = (c >> 2) & 1;
-        *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
-        *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
+        for (int it = 0; it < kLoads / 2; ++it) {
+          const int r = (i0 + it) * 4 * kRowsPer + r0;
+          const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+          uint4 y0, y1;
+          e4m3x4_f16(xw[0], y0.x, y0.y);
+          e4m3x4_f16(xw[1], y0.z, y0.w);
+          e4m3x4_f16(xw[2], y1.x, y1.y);
+          e4m3x4_f16(xw[3], y1.z, y1.w);
+          // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
+          uint8_t* at = dst + (c >> 2) * S::kHalf;
+          const int jx = (c & 3) * 2, up = (c >> 2) & 1;
+          *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
+          *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
+          x[it] = x[it + kLoads / 2];
+        }
       }
       fence_proxy_async_smem();
       mbar_arrive(&full[tile & 1]);
