@@ -186,10 +186,19 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
-// A whole warp's bounded wait: true for all its lanes or for none.
+// A whole warp's look at a barrier, and its bounded wait: true for all its lanes or for none.
+__device__ __forceinline__ bool warp_try(uint64_t* bar, uint32_t parity) {
+  return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
+}
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-  if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)), 1)) return true;
-  return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+  if (warp_try(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  bool more;
+  do {
+    if (warp_try(bar, parity)) return true;
+    more = global_timer_ns() - t0 < kWaitLimitNs;
+  } while (__all_sync(0xffffffffu, more));
+  return false;
 }
 
 template <int N>
@@ -657,145 +666,165 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       gr = R - j * a.G;
       t = j < cur.s.n ? cur.s.start + j : -1;
       cq = cqs[g * 128 + row];
-      for (int i = 0; i < jobs && ok; ++i) {
-        const uint32_t tile = tile0 + (uint32_t)(kPair ? i : 2 * i + g);
-        if (!warp_wait(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { ok = false; break; }
-        const TileMeta& meta = metas[tile % kMeta];
-        const bool whole = meta.whole != 0;
-        if (__builtin_expect(!whole, 0) && !warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u)) { ok = false; break; }   // the NaN flags
+      // 32 keys a step, in a short loop without rare cases: a wait that has to be waited for, keys that some row
+      // does not see, P out of its range and scales far apart leave the loop, are dealt with below it, and
+      // the step is taken up again.  (With those cases inside, the loop ran a quarter slower.)
+      // P is formed against the present maxima; where that leaves P's range (a sum above 60,000: a part's first keys,
+      // a new maximum), the maxima move.  So no maxima are taken of the scores before the exponentials, and none
+      // at all for most tiles.
+      constexpr int kU = 32 / kW;                        // scales of 32 keys
+      const int steps = 4 * jobs;
+      int c = 0;
+      bool seen = false, again = false;                  // the half tile's scores are there; its range has been seen to
+      for (;;) {
+        enum { kDone, kNoMeta, kNoScores, kHidden, kRange } why;
+        bool over;
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half, ++job) {
-          const uint32_t buf = job & 1u, sb = s_addr + 64u * buf;
-          if (!warp_wait(&bars->sfull[g][buf], (job >> 1) & 1u)) { ok = false; break; }
-          tc_fence_after();
-          if (__builtin_expect(!whole, 0)) hide(meta, half, tile, sb, t);
-          // 32 keys at a time: P against the present maxima; where that leaves P's range (above 2^15: a part's first
-          // keys, a new maximum), the maxima move and P is formed once more.  So the maxima are taken of P, in pairs,
-          // beside the exponentials, not of the scores before them.  The loops stay rolled and short: with the
-          // half tile unrolled the roles' code does not fit the innermost instruction cache.
-          constexpr int kU = 32 / kW;                    // scales in 32 keys
-#pragma unroll 1
-          for (int k = 0; k < 2 && ok; ++k) {
-            const int u0 = 4 * half + 2 * k;
-            float ls[kU], sums[kU];                      // log2 of the value scale, weights' sum per kW columns
-            uint32_t p[16];
-            bool far = false;
-#pragma unroll 1
-            for (int again = 0;; ++again) {
-              float x[32], fs[kU];
-              __syncwarp();
-              tmem_ld_32x32b_x32(sb + 32u * k, x);
-#pragma unroll
-              for (int v = 0; v < kU; ++v) {
-                fs[v] = fmaxf(fminf(meta.ks[u0 + v] * cq, 3.0e38f), 1.2e-38f);
-                ls[v] = meta.lv[u0 + v];
-              }
-              const float lv_min = meta.lv_min[half];
-              tmem_wait_ld();
-              __half2 top = __float2half2_rn(0.f);
-#pragma unroll
-              for (int v = 0; v < kU; ++v) {
-                const float* xs = x + kW * v;
-                const float b = ls[v] - mw + kShift;
-                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-                const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
-#pragma unroll
-                for (int c = 0; c < kW; c += 4) {
-                  float2 y0 = fma2(make_float2(xs[c], xs[c + 1]), f2, b2);
-                  float2 y1 = fma2(make_float2(xs[c + 2], xs[c + 3]), f2, b2);
-                  y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
-                  s0 = add2(s0, y0);
-                  s1 = add2(s1, y1);
-                  const __half2 h0 = __floats2half2_rn(y0.x, y0.y), h1 = __floats2half2_rn(y1.x, y1.y);
-                  top = __hmax2(top, __hmax2(h0, h1));
-                  p[(kW * v + c) / 2] = *reinterpret_cast<const uint32_t*>(&h0);
-                  p[(kW * v + c) / 2 + 1] = *reinterpret_cast<const uint32_t*>(&h1);
-                }
-                s0 = add2(s0, s1);
-                sums[v] = s0.x + s0.y;
-              }
-              if (again) break;
-              const bool over = fmaxf(__low2float(top), __high2float(top)) > 32768.f;
-              far = mw - mz - kShift - lv_min > 80.f;
-              if (__builtin_expect(!__any_sync(0xffffffffu, over || far), 1)) break;
-              far = true;
-              if (!__any_sync(0xffffffffu, over)) break;
-              float cz = -INFINITY, cw = -INFINITY;
-#pragma unroll 1
-              for (int u = 0; u < 2; ++u) {
-                float y[16];
-                tmem_ld_32x32b_x16(sb + 32u * k + 16u * u, y);
-                tmem_wait_ld();
-                float m16 = y[0];
-#pragma unroll
-                for (int c = 1; c < 16; ++c) m16 = fmaxf(m16, y[c]);
-                const float zt = m16 * fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
-                cz = fmaxf(cz, zt);
-                cw = fmaxf(cw, zt + meta.lv[u0 + u]);
-              }
-              const float nw = over ? fmaxf(mw, cw) : mw, nz = over ? fmaxf(mz, cz) : mz;
-              const float al = ex2(mw - nw);
-              l *= ex2(mz - nz);
-              mw = nw;
-              mz = nz;
-              if (k > 0) {                               // the half tile's first P
-                float y[16];
-                uint32_t yw[16];
-                tmem_ld_32x32b_x16(sb, y);
-                tmem_wait_ld();
-                const __half2 a2 = __float2half2_rn(al);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) {
-                  const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[q]), a2);
-                  yw[q] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                tmem_st_32x32b_x16(sb, yw);
-              }
-              if (i + half > 0) {                        // O, once the group's last product is complete
-                if (!warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u)) { ok = false; break; }
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D; c += 16) {
-                  float o[16];
-                  tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
-                  tmem_wait_ld();
-                  uint32_t ow[16];
-#pragma unroll
-                  for (int q = 0; q < 16; ++q) ow[q] = __float_as_uint(o[q] * al);
-                  tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
-                }
-              }
-            }
-            const float back0 = mw - mz - kShift;
-            if (__builtin_expect(far, 0)) {
-              // denominators whose factor is out of range: their exponentials apart
-#pragma unroll 1
-              for (int u = 0; u < 2; ++u) {
-                float y[16];
-                __syncwarp();
-                tmem_ld_32x32b_x16(sb + 32u * k + 16u * u, y);
-                tmem_wait_ld();
-                const float fq = fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
-                if (back0 - meta.lv[u0 + u] > 80.f) {
-#pragma unroll
-                  for (int c = 0; c < 16; ++c) l += ex2(y[c] * fq - mz);
-                }
-              }
-            }
-#pragma unroll
-            for (int v = 0; v < kU; ++v) {
-              const float back = back0 - ls[v];
-              if (!(back > 80.f)) l = fmaf(sums[v], ex2(back), l);
-            }
-            __syncwarp();
-            tmem_st_32x32b_x16(sb + 16u * k, p);         // over columns of S that have been read
+        for (;;) {
+          if (c == steps) { why = kDone; break; }
+          const uint32_t tile = tile0 + (uint32_t)(kPair ? c >> 2 : 2 * (c >> 2) + g), buf = job & 1u;
+          const uint32_t sb = s_addr + 64u * buf;
+          const TileMeta& meta = metas[tile % kMeta];
+          if (!seen) {
+            if ((c & 3) == 0 && !warp_try(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { why = kNoMeta; break; }
+            if (!warp_try(&bars->sfull[g][buf], (job >> 1) & 1u)) { why = kNoScores; break; }
+            tc_fence_after();
+            if (!meta.whole) { why = kHidden; break; }
           }
-          if (!ok) break;
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(&bars->pfull[g][buf]);
+          float x[32], fs[kU], ls[kU], sums[kU];         // scores; logit factor, log2 of the value scale, sum per kW keys
+          uint32_t p[16];
+          __syncwarp();
+          tmem_ld_32x32b_x32(sb + 32u * (c & 1), x);
+          const int u0 = 2 * (c & 3);
+#pragma unroll
+          for (int v = 0; v < kU; ++v) {
+            fs[v] = fmaxf(fminf(meta.ks[u0 + v] * cq, 3.0e38f), 1.2e-38f);
+            ls[v] = meta.lv[u0 + v];
+          }
+          const float back0 = mw - mz - kShift;
+          const bool far = back0 - meta.lv_min[(c >> 1) & 1] > 80.f;
+          tmem_wait_ld();
+          over = false;
+#pragma unroll
+          for (int v = 0; v < kU; ++v) {
+            const float* xs = x + kW * v;
+            const float b = ls[v] - mw + kShift;
+            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+            const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
+#pragma unroll
+            for (int q = 0; q < kW; q += 4) {
+              float2 y0 = fma2(make_float2(xs[q], xs[q + 1]), f2, b2);
+              float2 y1 = fma2(make_float2(xs[q + 2], xs[q + 3]), f2, b2);
+              y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+              s0 = add2(s0, y0);
+              s1 = add2(s1, y1);
+              p[(kW * v + q) / 2] = pack_f16x2(y0.x, y0.y);
+              p[(kW * v + q) / 2 + 1] = pack_f16x2(y1.x, y1.y);
+            }
+            s0 = add2(s0, s1);
+            sums[v] = s0.x + s0.y;
+            over |= sums[v] > 60000.f;
+          }
+          if (__any_sync(0xffffffffu, over || far) && !again) { why = kRange; break; }
+#pragma unroll
+          for (int v = 0; v < kU; ++v) {
+            const float back = back0 - ls[v];
+            if (!(back > 80.f)) l = fmaf(sums[v], ex2(back), l);
+          }
+          tmem_st_32x32b_x16(sb + 16u * (c & 1), p);     // over columns of S that have been read
+          if (c & 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->pfull[g][buf]);
+            ++job;
+          }
+          if ((c & 3) == 3 && lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
+          again = false;
+          seen = (c & 1) == 0;
+          ++c;
         }
-        if (lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
+        if (why == kDone) break;
+        const uint32_t tile = tile0 + (uint32_t)(kPair ? c >> 2 : 2 * (c >> 2) + g), buf = job & 1u;
+        const uint32_t sb = s_addr + 64u * buf;
+        const TileMeta& meta = metas[tile % kMeta];
+        if (why == kNoMeta) {
+          ok = warp_wait(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u);
+        } else if (why == kNoScores) {
+          ok = warp_wait(&bars->sfull[g][buf], (job >> 1) & 1u);
+        } else if (why == kHidden) {
+          ok = warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u);            // the NaN flags
+          if (ok) hide(meta, (c >> 1) & 1, tile, sb, t);
+          seen = true;
+        } else {
+          const int u0 = 2 * (c & 3);
+          const uint32_t sk = sb + 32u * (c & 1);
+          if (__any_sync(0xffffffffu, over)) {
+            float cz = -INFINITY, cw = -INFINITY;
+#pragma unroll 1
+            for (int u = 0; u < 2; ++u) {
+              float y[16];
+              tmem_ld_32x32b_x16(sk + 16u * u, y);
+              tmem_wait_ld();
+              float m16 = y[0];
+#pragma unroll
+              for (int q = 1; q < 16; ++q) m16 = fmaxf(m16, y[q]);
+              const float zt = m16 * fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
+              cz = fmaxf(cz, zt);
+              cw = fmaxf(cw, zt + meta.lv[u0 + u]);
+            }
+            // a maximum moves where a key exceeds it by more than 8; the others' P fit as they are
+            const bool move = cw > mw + 8.f;
+            const float nw = move ? cw : mw, nz = move ? fmaxf(mz, cz) : mz, al = ex2(mw - nw);
+            l *= ex2(mz - nz);
+            mw = nw;
+            mz = nz;
+            if (c & 1) {                                 // the half tile's first P
+              float y[16];
+              uint32_t yw[16];
+              tmem_ld_32x32b_x16(sb, y);
+              tmem_wait_ld();
+              const __half2 a2 = __float2half2_rn(al);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) {
+                const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[q]), a2);
+                yw[q] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+              tmem_st_32x32b_x16(sb, yw);
+            }
+            if (c > 1) {                                 // O, once the group's last product is complete
+              ok = warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u);
+              tc_fence_after();
+#pragma unroll 1
+              for (int q = 0; q < D; q += 16) {
+                float o[16];
+                tmem_ld_32x32b_x16(o_addr + (uint32_t)q, o);
+                tmem_wait_ld();
+                uint32_t ow[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) ow[e] = __float_as_uint(o[e] * al);
+                tmem_st_32x32b_x16(o_addr + (uint32_t)q, ow);
+              }
+              tmem_wait_st();
+            }
+          }
+          // denominators whose factor is out of range: their exponentials apart
+          const float back0 = mw - mz - kShift;
+#pragma unroll 1
+          for (int u = 0; u < 2; ++u) {
+            float y[16];
+            __syncwarp();
+            tmem_ld_32x32b_x16(sk + 16u * u, y);
+            tmem_wait_ld();
+            const float fq = fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
+            if (back0 - meta.lv[u0 + u] > 80.f) {
+#pragma unroll
+              for (int q = 0; q < 16; ++q) l += ex2(y[q] * fq - mz);
+            }
+          }
+          __syncwarp();
+          seen = again = true;
+        }
+        if (!ok) break;
       }
       tile0 += (uint32_t)cur.tiles;
       if (!ok) break;
@@ -816,50 +845,84 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const uint8_t* pool = is_v ? a.P.v : a.P.k;
     bool ok = true;
     uint4 x[kLoads];
-    bool masked = false;
-    uint32_t have = 0;
-    // the codes of tile n into registers
-    auto load = [&](uint32_t n) {
-      if (!warp_wait(&bars->mfull[n % kMeta], (n / kMeta) & 1u)) return false;
-      const TileMeta& m = metas[n % kMeta];
-      masked = m.whole == 0;
-      have = m.have;
-      int32_t pg[kSubs];
-      *reinterpret_cast<int4*>(pg) = *reinterpret_cast<const int4*>(m.page);
-      *reinterpret_cast<int4*>(pg + 4) = *reinterpret_cast<const int4*>(m.page + 4);
-      const uint8_t* base = pool + (size_t)m.h * a.T.page * D + 16 * c;
-      const int at = m.pos + r0, inside = a.T.page - 1;
-      const size_t per = (size_t)a.Hkv * a.T.page * D;
-#pragma unroll
-      for (int it = 0; it < kLoads; ++it) {
-        // rows without a page read page 0 (and are cleared below)
-        const int r = it * 4 * kRowsPer;
-        const int32_t p0 = pg[r >> 4], p1 = pg[(r >> 4) + (kRowsPer == 8 ? 1 : 0)];
-        const int32_t p = kRowsPer == 8 && w >= 2 ? p1 : p0;
-        x[it] = *reinterpret_cast<const uint4*>(base + (size_t)(p < 0 ? 0 : p) * per + (size_t)((at + r) & inside) * D);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars->mfree[n % kMeta]);
-      return true;
-    };
+    uint32_t have = 0, tile = 0;
     const uint32_t total = (uint32_t)run_tiles;
-    ok = load(0);
-    for (uint32_t tile = 0; tile < total && ok; ++tile) {
-      if (!warp_wait(&freeb[tile & 1], ((tile >> 1) & 1u) ^ 1u)) { ok = false; break; }
-      uint8_t* dst = tiles + (tile & 1) * S::kTileBytes;
-      if (is_v && masked) {
+    const uint8_t* lane_base = pool + 16 * c;
+    const size_t per_head = (size_t)a.T.page * D, per_page = per_head * a.Hkv;
+    const int inside = a.T.page - 1;
+    bool loaded = false, clean = false;                       // x holds the tile's codes; without NaN codes, where it matters
+    for (;;) {
+      enum { kDone, kNoMeta, kNoRoom, kMasked } why;          // as above: the loop without its rare cases
+#pragma unroll 1
+      for (;;) {
+        if (!loaded) {
+          if (!warp_try(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { why = kNoMeta; break; }
+          const TileMeta& m = metas[tile % kMeta];
+          clean = !is_v || m.whole;
+          have = m.have;
+          int32_t pg[kSubs];
+          *reinterpret_cast<int4*>(pg) = *reinterpret_cast<const int4*>(m.page);
+          *reinterpret_cast<int4*>(pg + 4) = *reinterpret_cast<const int4*>(m.page + 4);
+          const uint8_t* base = lane_base + m.h * per_head;
+          const int at = m.pos + r0;
+#pragma unroll
+          for (int it = 0; it < kLoads; ++it) {
+            // rows without a page read page 0 (V's are cleared below, K's scores hidden)
+            const int r = it * 4 * kRowsPer;
+            const int32_t p0 = pg[r >> 4], p1 = pg[(r >> 4) + (kRowsPer == 8 ? 1 : 0)];
+            const int32_t p = kRowsPer == 8 && w >= 2 ? p1 : p0;
+            x[it] = *reinterpret_cast<const uint4*>(base + (size_t)(p < 0 ? 0 : p) * per_page + (size_t)((at + r) & inside) * D);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
+          loaded = true;
+        }
+        if (!warp_try(&freeb[tile & 1], ((tile >> 1) & 1u) ^ 1u)) { why = kNoRoom; break; }
+        if (!clean) { why = kMasked; break; }
+        uint8_t* dst = tiles + (tile & 1) * S::kTileBytes;
+#pragma unroll 1
+        for (int i0 = 0; i0 < kLoads; i0 += kLoads / 2) {
+#pragma unroll
+          for (int it = 0; it < kLoads / 2; ++it) {
+            const int r = (i0 + it) * 4 * kRowsPer + r0;
+            const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+            uint4 y0, y1;
+            e4m3x4_f16(xw[0], y0.x, y0.y);
+            e4m3x4_f16(xw[1], y0.z, y0.w);
+            e4m3x4_f16(xw[2], y1.x, y1.y);
+            e4m3x4_f16(xw[3], y1.z, y1.w);
+            // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
+            uint8_t* at = dst + (c >> 2) * S::kHalf;
+            const int jx = (c & 3) * 2, up = (c >> 2) & 1;
+            *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
+            *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
+            x[it] = x[it + kLoads / 2];
+          }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&full[tile & 1]);
+        loaded = false;
+        if (++tile == total) { why = kDone; break; }
+      }
+      if (why == kDone) break;
+      if (why == kNoMeta) {
+        ok = warp_wait(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u);
+      } else if (why == kNoRoom) {
+        ok = warp_wait(&freeb[tile & 1], ((tile >> 1) & 1u) ^ 1u);
+      } else {
         // some row does not see some key: NaN codes become 0 and are flagged for the rows that do
 #pragma unroll
         for (int it = 0; it < kLoads; ++it) {
-          uint32_t* xw = reinterpret_cast<uint32_t*>(&x[it]);
-          uint32_t any = 0;
           if (!((have >> ((it * 4 * kRowsPer + r0) >> 4)) & 1u)) x[it] = make_uint4(0u, 0u, 0u, 0u);
+          uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+          uint32_t any = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             const uint32_t nb = nan_bytes(xw[q]);
             any |= nb;
             xw[q] &= ~((nb >> 7) * 0xFFu);
           }
+          x[it] = make_uint4(xw[0], xw[1], xw[2], xw[3]);
           const uint32_t bal = __ballot_sync(0xffffffffu, any != 0);
           // four rows to a byte
           if (lane < kRowsPer / 4) {
@@ -869,30 +932,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               fl |= ((bal >> ((4 * lane + q) * kLanes)) & ((1u << kLanes) - 1u)) ? 1u << q : 0u;
             nans[(tile & 1) * 32 + (it * 4 * kRowsPer + w * kRowsPer) / 4 + lane] = (uint8_t)fl;
           }
+          __syncwarp();
         }
+        clean = true;
       }
-#pragma unroll 1
-      for (int i0 = 0; i0 < kLoads; i0 += kLoads / 2) {
-#pragma unroll
-        for (int it = 0; it < kLoads / 2; ++it) {
-          const int r = (i0 + it) * 4 * kRowsPer + r0;
-          const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
-          uint4 y0, y1;
-          e4m3x4_f16(xw[0], y0.x, y0.y);
-          e4m3x4_f16(xw[1], y0.z, y0.w);
-          e4m3x4_f16(xw[2], y1.x, y1.y);
-          e4m3x4_f16(xw[3], y1.z, y1.w);
-          // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
-          uint8_t* at = dst + (c >> 2) * S::kHalf;
-          const int jx = (c & 3) * 2, up = (c >> 2) & 1;
-          *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
-          *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
-          x[it] = x[it + kLoads / 2];
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&full[tile & 1]);
-      if (tile + 1 < total) ok = load(tile + 1);
+      if (!ok) break;
     }
     if (!ok) set_device_error(a.err, kErrWaitTimeout);
   }
