@@ -38,7 +38,7 @@ constexpr int kThreads = 640;
 constexpr int kSubs = kKeys / 16;
 constexpr int kMeta = 8;                        // tiles looked up ahead, four at a time
 constexpr float kShift = 7.f;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsConvert = 72, kRegsIssue = 80;
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 64;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
 
 struct __align__(8) TcBars {
@@ -666,14 +666,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       gr = R - j * a.G;
       t = j < cur.s.n ? cur.s.start + j : -1;
       cq = cqs[g * 128 + row];
-      // 32 keys a step, in a short loop without rare cases: a wait that has to be waited for, keys that some row
+      // A half tile a step, in a short loop without rare cases: a wait that has to be waited for, keys that some row
       // does not see, P out of its range and scales far apart leave the loop, are dealt with below it, and
       // the step is taken up again.  (With those cases inside, the loop ran a quarter slower.)
       // P is formed against the present maxima; where that leaves P's range (a sum above 60,000: a part's first keys,
       // a new maximum), the maxima move.  So no maxima are taken of the scores before the exponentials, and none
       // at all for most tiles.
-      constexpr int kU = 32 / kW;                        // scales of 32 keys
-      const int steps = 4 * jobs;
+      constexpr int kU = 64 / kW;                        // scales of a half tile
+      const int steps = 2 * jobs;
       int c = 0;
       bool seen = false, again = false;                  // the half tile's scores are there; its range has been seen to
       for (;;) {
@@ -682,27 +682,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
 #pragma unroll 1
         for (;;) {
           if (c == steps) { why = kDone; break; }
-          const uint32_t tile = tile0 + (uint32_t)(kPair ? c >> 2 : 2 * (c >> 2) + g), buf = job & 1u;
+          const uint32_t tile = tile0 + (uint32_t)(kPair ? c >> 1 : 2 * (c >> 1) + g), buf = job & 1u;
           const uint32_t sb = s_addr + 64u * buf;
           const TileMeta& meta = metas[tile % kMeta];
           if (!seen) {
-            if ((c & 3) == 0 && !warp_try(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { why = kNoMeta; break; }
+            if ((c & 1) == 0 && !warp_try(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { why = kNoMeta; break; }
             if (!warp_try(&bars->sfull[g][buf], (job >> 1) & 1u)) { why = kNoScores; break; }
             tc_fence_after();
             if (!meta.whole) { why = kHidden; break; }
           }
-          float x[32], fs[kU], ls[kU], sums[kU];         // scores; logit factor, log2 of the value scale, sum per kW keys
-          uint32_t p[16];
+          float x[64], fs[kU], ls[kU], sums[kU];         // scores; logit factor, log2 of the value scale, sum per kW keys
+          uint32_t p[32];
           __syncwarp();
-          tmem_ld_32x32b_x32(sb + 32u * (c & 1), x);
-          const int u0 = 2 * (c & 3);
+          tmem_ld_32x32b_x32(sb, x);
+          tmem_ld_32x32b_x32(sb + 32u, x + 32);
+          const int u0 = 4 * (c & 1);
 #pragma unroll
           for (int v = 0; v < kU; ++v) {
-            fs[v] = fmaxf(fminf(meta.ks[u0 + v] * cq, 3.0e38f), 1.2e-38f);
-            ls[v] = meta.lv[u0 + v];
+            fs[v] = fmaxf(fminf(meta.ks[u0 + v * (kW / 16)] * cq, 3.0e38f), 1.2e-38f);
+            ls[v] = meta.lv[u0 + v * (kW / 16)];
           }
           const float back0 = mw - mz - kShift;
-          const bool far = back0 - meta.lv_min[(c >> 1) & 1] > 80.f;
+          const bool far = back0 - meta.lv_min[c & 1] > 80.f;
           tmem_wait_ld();
           over = false;
 #pragma unroll
@@ -731,20 +732,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             const float back = back0 - ls[v];
             if (!(back > 80.f)) l = fmaf(sums[v], ex2(back), l);
           }
-          tmem_st_32x32b_x16(sb + 16u * (c & 1), p);     // over columns of S that have been read
-          if (c & 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            mbar_arrive(&bars->pfull[g][buf]);
-            ++job;
-          }
-          if ((c & 3) == 3 && lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
-          again = false;
-          seen = (c & 1) == 0;
+          tmem_st_32x32b_x16(sb, p);
+          tmem_st_32x32b_x16(sb + 16u, p + 16);
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->pfull[g][buf]);
+          if ((c & 1) && lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
+          seen = again = false;
+          ++job;
           ++c;
         }
         if (why == kDone) break;
-        const uint32_t tile = tile0 + (uint32_t)(kPair ? c >> 2 : 2 * (c >> 2) + g), buf = job & 1u;
+        const uint32_t tile = tile0 + (uint32_t)(kPair ? c >> 1 : 2 * (c >> 1) + g), buf = job & 1u;
         const uint32_t sb = s_addr + 64u * buf;
         const TileMeta& meta = metas[tile % kMeta];
         if (why == kNoMeta) {
@@ -753,17 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           ok = warp_wait(&bars->sfull[g][buf], (job >> 1) & 1u);
         } else if (why == kHidden) {
           ok = warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u);            // the NaN flags
-          if (ok) hide(meta, (c >> 1) & 1, tile, sb, t);
+          if (ok) hide(meta, c & 1, tile, sb, t);
           seen = true;
         } else {
-          const int u0 = 2 * (c & 3);
-          const uint32_t sk = sb + 32u * (c & 1);
+          const int u0 = 4 * (c & 1);
           if (__any_sync(0xffffffffu, over)) {
             float cz = -INFINITY, cw = -INFINITY;
 #pragma unroll 1
-            for (int u = 0; u < 2; ++u) {
+            for (int u = 0; u < 4; ++u) {
               float y[16];
-              tmem_ld_32x32b_x16(sk + 16u * u, y);
+              tmem_ld_32x32b_x16(sb + 16u * u, y);
               tmem_wait_ld();
               float m16 = y[0];
 #pragma unroll
@@ -778,20 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             l *= ex2(mz - nz);
             mw = nw;
             mz = nz;
-            if (c & 1) {                                 // the half tile's first P
-              float y[16];
-              uint32_t yw[16];
-              tmem_ld_32x32b_x16(sb, y);
-              tmem_wait_ld();
-              const __half2 a2 = __float2half2_rn(al);
-#pragma unroll
-              for (int q = 0; q < 16; ++q) {
-                const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[q]), a2);
-                yw[q] = *reinterpret_cast<const uint32_t*>(&h);
-              }
-              tmem_st_32x32b_x16(sb, yw);
-            }
-            if (c > 1) {                                 // O, once the group's last product is complete
+            if (c > 0) {                                 // O, once the group's last product is complete
               ok = warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u);
               tc_fence_after();
 #pragma unroll 1
@@ -810,10 +795,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           // denominators whose factor is out of range: their exponentials apart
           const float back0 = mw - mz - kShift;
 #pragma unroll 1
-          for (int u = 0; u < 2; ++u) {
+          for (int u = 0; u < 4; ++u) {
             float y[16];
             __syncwarp();
-            tmem_ld_32x32b_x16(sk + 16u * u, y);
+            tmem_ld_32x32b_x16(sb + 16u * u, y);
             tmem_wait_ld();
             const float fq = fmaxf(fminf(meta.ks[u0 + u] * cq, 3.0e38f), 1.2e-38f);
             if (back0 - meta.lv[u0 + u] > 80.f) {
