@@ -206,6 +206,13 @@ def _tensor(t, name, dtypes, shape):
         raise CsaError(1, f"{name} is not contiguous")
 
 
+def _one_device(*tensors):
+    d = tensors[0].get_device()
+    if any(t.get_device() != d for t in tensors):
+        raise CsaError(1, "tensors on different devices: " + ", ".join(str(t.device) for t in tensors))
+    return d
+
+
 def make_page_pool(k, v, k_scale, v_scale) -> CsaPagePool:
     """Page pool struct over codes [n_pages, Hkv, page, D] (uint8 or float8_e4m3fn) and scales [n_pages, Hkv]
     (float32).  It keeps the tensors alive."""
@@ -215,7 +222,7 @@ def make_page_pool(k, v, k_scale, v_scale) -> CsaPagePool:
     _tensor(k_scale, "k_scale", (torch.float32,), tuple(k.shape[:2]))
     _tensor(v_scale, "v_scale", (torch.float32,), tuple(k.shape[:2]))
     p = CsaPagePool(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr())
-    p.shape, p.keep = tuple(k.shape), (k, v, k_scale, v_scale)
+    p.shape, p.keep, p.device = tuple(k.shape), (k, v, k_scale, v_scale), _one_device(k, v, k_scale, v_scale)
     return p
 
 
@@ -224,7 +231,7 @@ def make_page_table(table, refs, page) -> CsaPageTable:
     _tensor(table, "table", (torch.int32,), (None, None))
     _tensor(refs, "refs", (torch.int32,), (None,))
     t = CsaPageTable(table.data_ptr(), refs.data_ptr(), table.shape[1], refs.shape[0], table.shape[0], page)
-    t.keep = (table, refs)
+    t.keep, t.device = (table, refs), _one_device(table, refs)
     return t
 
 
@@ -412,41 +419,56 @@ def csa_attend_merge(L, params, q_pos, parts, partials, out, stream=None):
 
 
 # ----------------------------------------------------------------------------- paged 8-bit cache
+# These calls run once per layer and token, and their kernels take microseconds: the checks are kept to one
+# look at each tensor, and pointers go to the library as plain numbers.
 _ACT = {0: torch.float32, 1: torch.bfloat16}
+
+
+def _here(T):
+    """The device of the table's tensors, which has to be the current one (a kernel elsewhere could not read them)."""
+    d = T.device
+    if d < 0 or d != torch.cuda.current_device():
+        raise CsaError(1, f"the page table is on device {d} (-1: the CPU), not on the current device")
+    return d
+
+
+def _arg(t, name, dtype, n, d):
+    """Address of a contiguous tensor of at least n values on device d; None for None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.numel() < n or not t.is_contiguous() or t.get_device() != d:
+        raise CsaError(1, f"{name} must be {n} contiguous {dtype} on device {d}")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, d):
+    return torch._C._cuda_getCurrentRawStream(d) if stream is None else stream.cuda_stream
 
 
 def _paged_pool(G, pool, T):
     """Refuses a pool that is not the layer's or not the table's."""
     if pool.shape != (T.n_pages, G.Hkv, T.page, G.D):
         raise CsaError(1, f"pool of {pool.shape}, not {(T.n_pages, G.Hkv, T.page, G.D)} as the layer and the table say")
+    if pool.device != T.device:
+        raise CsaError(1, f"the pool is on device {pool.device}, the table on device {T.device}")
 
 
-def _ints(t, name, dtype, n):
-    if t is not None and (t.dtype != dtype or t.numel() < n or not t.is_contiguous()):
-        raise CsaError(1, f"{name} must be {n} contiguous {dtype}")
-
-
-def _on_device(T, *tensors):
-    """Refuses tensors that are not all on the current device (a kernel there could not read them)."""
-    d = torch.cuda.current_device()
-    for t in (*T.keep, *tensors):
-        if t is not None and (not t.is_cuda or t.get_device() != d):
-            raise CsaError(1, f"a tensor is on {t.device}, not on the current device cuda:{d}")
-
-
-def _token_stride(t, name, G, B, Tq, heads):
+def _token_stride(t, name, G, B, Tq, heads, d=None):
     """Elements between the tokens of t [B, Tq, heads, D] (or [B, Tq, heads * D]), each token contiguous."""
-    if t.dtype != _ACT.get(G.act_format):
+    if t.dtype is not _ACT.get(G.act_format):
         raise CsaError(1, f"{name} is {t.dtype}, not the layer's activation type")
+    if d is not None and t.get_device() != d:
+        raise CsaError(1, f"{name} is on {t.device}, not on device {d}")
+    D = G.D
     shape, st = tuple(t.shape), t.stride()
-    if shape == (B, Tq, heads, G.D):
-        inner = (st[3] == 1 or G.D == 1) and (st[2] == G.D or heads == 1)
-    elif shape == (B, Tq, heads * G.D):
+    if shape == (B, Tq, heads, D):
+        inner = st[3] == 1 and (st[2] == D or heads == 1)
+    elif shape == (B, Tq, heads * D):
         inner = st[2] == 1
     else:
-        raise CsaError(1, f"{name} has shape {shape}, not {(B, Tq, heads, G.D)}")
-    step = st[1] if Tq > 1 else (st[0] if B > 1 else heads * G.D)
-    if not inner or step < heads * G.D or (B > 1 and st[0] != Tq * step):
+        raise CsaError(1, f"{name} has shape {shape}, not {(B, Tq, heads, D)}")
+    step = st[1] if Tq > 1 else (st[0] if B > 1 else heads * D)
+    if not inner or step < heads * D or (B > 1 and st[0] != Tq * step):
         raise CsaError(1, f"{name}: tokens must be contiguous rows at one distance from each other")
     return step
 
@@ -454,75 +476,63 @@ def _token_stride(t, name, G, B, Tq, heads):
 def csa_paged_append(G, pool, T, k_new, v_new, start, n_new, Tq, stream=None):
     """k_new, v_new: [B, Tq, Hkv, D]; a view whose tokens lie at one distance (a slice of a fused projection) is
     taken as it is."""
+    d, B = _here(T), T.B
     _paged_pool(G, pool, T)
-    stride = _token_stride(k_new, "k_new", G, T.B, Tq, G.Hkv)
-    if _token_stride(v_new, "v_new", G, T.B, Tq, G.Hkv) != stride:
+    stride = _token_stride(k_new, "k_new", G, B, Tq, G.Hkv, d)
+    if _token_stride(v_new, "v_new", G, B, Tq, G.Hkv, d) != stride:
         raise CsaError(1, "k_new and v_new have tokens at different distances")
-    _ints(start, "start", torch.int64, T.B)
-    _ints(n_new, "n_new", torch.int32, T.B)
-    _on_device(T, *pool.keep, k_new, v_new, start, n_new)
-    _check(lib().csa_paged_append(ctypes.byref(G), ctypes.byref(pool), ctypes.byref(T), ptr(k_new), ptr(v_new), stride,
-                                  ptr(start), ptr(n_new), Tq, _stream(stream)))
+    _check(lib().csa_paged_append(G, pool, T, k_new.data_ptr(), v_new.data_ptr(), stride,
+                                  _arg(start, "start", torch.int64, B, d), _arg(n_new, "n_new", torch.int32, B, d), Tq,
+                                  _raw_stream(stream, d)))
 
 
 def csa_paged_workspace_size(G, T, Tq, n_max) -> int:
-    return lib().csa_paged_workspace_size(ctypes.byref(G), ctypes.byref(T), Tq, n_max)
+    return lib().csa_paged_workspace_size(G, T, Tq, n_max)
 
 
 def csa_paged_attend(G, pool, T, q, sinks, start, n_new, Tq, n_max, out, workspace, stream=None):
     """q: [B, Tq, H, D] (tokens at one distance from each other); out: [B, Tq, H, D], contiguous."""
+    d, B, H = _here(T), T.B, G.H
     _paged_pool(G, pool, T)
-    stride = _token_stride(q, "q", G, T.B, Tq, G.H)
-    if _token_stride(out, "out", G, T.B, Tq, G.H) != G.H * G.D:
+    stride = _token_stride(q, "q", G, B, Tq, H, d)
+    if _token_stride(out, "out", G, B, Tq, H, d) != H * G.D:
         raise CsaError(1, "out must be contiguous")
-    _ints(start, "start", torch.int64, T.B)
-    _ints(n_new, "n_new", torch.int32, T.B)
-    _ints(sinks, "sinks", torch.float32, G.H)
-    _on_device(T, *pool.keep, q, sinks, start, n_new, out, workspace)
-    _check(lib().csa_paged_attend(ctypes.byref(G), ctypes.byref(pool), ctypes.byref(T), ptr(q), stride, ptr(sinks),
-                                  ptr(start), ptr(n_new), Tq, n_max, ptr(out), ptr(workspace),
-                                  workspace.numel() * workspace.element_size(), _stream(stream)))
+    if workspace.get_device() != d:
+        raise CsaError(1, f"the workspace is on {workspace.device}, not on device {d}")
+    _check(lib().csa_paged_attend(G, pool, T, q.data_ptr(), stride, _arg(sinks, "sinks", torch.float32, H, d),
+                                  _arg(start, "start", torch.int64, B, d), _arg(n_new, "n_new", torch.int32, B, d), Tq,
+                                  n_max, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                  _raw_stream(stream, d)))
 
 
 def csa_pages_fork(T, src, dst, n, stream=None):
-    _ints(src, "src", torch.int32, n)
-    _ints(dst, "dst", torch.int32, n)
-    _on_device(T, src, dst)
-    _check(lib().csa_pages_fork(ctypes.byref(T), ptr(src), ptr(dst), n, _stream(stream)))
+    d = _here(T)
+    _check(lib().csa_pages_fork(T, _arg(src, "src", torch.int32, n, d), _arg(dst, "dst", torch.int32, n, d), n,
+                                _raw_stream(stream, d)))
 
 
 def csa_pages_reserve(T, start, n_new, Tq, copy_src, copy_dst, missing, stream=None):
-    _ints(start, "start", torch.int64, T.B)
-    _ints(n_new, "n_new", torch.int32, T.B)
-    _ints(copy_src, "copy_src", torch.int32, T.B)
-    _ints(copy_dst, "copy_dst", torch.int32, T.B)
-    _ints(missing, "missing", torch.int32, 1)
-    _on_device(T, start, n_new, copy_src, copy_dst, missing)
-    _check(lib().csa_pages_reserve(ctypes.byref(T), ptr(start), ptr(n_new), Tq, ptr(copy_src), ptr(copy_dst),
-                                   ptr(missing), _stream(stream)))
+    d, B, i32 = _here(T), T.B, torch.int32
+    _check(lib().csa_pages_reserve(T, _arg(start, "start", torch.int64, B, d), _arg(n_new, "n_new", i32, B, d), Tq,
+                                   _arg(copy_src, "copy_src", i32, B, d), _arg(copy_dst, "copy_dst", i32, B, d),
+                                   _arg(missing, "missing", i32, 1, d), _raw_stream(stream, d)))
 
 
 def csa_pages_free(T, keep, begin, first, stream=None):
-    _ints(keep, "keep", torch.int64, T.B)
-    _ints(begin, "begin", torch.int64, T.B)
-    _on_device(T, keep, begin)
-    _check(lib().csa_pages_free(ctypes.byref(T), ptr(keep), ptr(begin), first, _stream(stream)))
+    d, B = _here(T), T.B
+    _check(lib().csa_pages_free(T, _arg(keep, "keep", torch.int64, B, d), _arg(begin, "begin", torch.int64, B, d), first,
+                                _raw_stream(stream, d)))
 
 
 def csa_pages_compact(T, max_moves, move_src, move_dst, count, stream=None):
-    _ints(move_src, "move_src", torch.int32, max_moves)
-    _ints(move_dst, "move_dst", torch.int32, max_moves)
-    _ints(count, "count", torch.int32, 1)
-    _on_device(T, move_src, move_dst, count)
-    _check(lib().csa_pages_compact(ctypes.byref(T), max_moves, ptr(move_src), ptr(move_dst), ptr(count),
-                                   _stream(stream)))
+    d, i32 = _here(T), torch.int32
+    _check(lib().csa_pages_compact(T, max_moves, _arg(move_src, "move_src", i32, max_moves, d),
+                                   _arg(move_dst, "move_dst", i32, max_moves, d), _arg(count, "count", i32, 1, d),
+                                   _raw_stream(stream, d)))
 
 
 def csa_pages_copy(G, pool, T, src, dst, count, n, stream=None):
+    d, i32 = _here(T), torch.int32
     _paged_pool(G, pool, T)
-    _ints(src, "src", torch.int32, n)
-    _ints(dst, "dst", torch.int32, n)
-    _ints(count, "count", torch.int32, 1)
-    _on_device(T, *pool.keep, src, dst, count)
-    _check(lib().csa_pages_copy(ctypes.byref(G), ctypes.byref(pool), ctypes.byref(T), ptr(src), ptr(dst), ptr(count), n,
-                                _stream(stream)))
+    _check(lib().csa_pages_copy(G, pool, T, _arg(src, "src", i32, n, d), _arg(dst, "dst", i32, n, d),
+                                _arg(count, "count", i32, 1, d), n, _raw_stream(stream, d)))

@@ -1,4 +1,5 @@
 // C ABI of the paged 8-bit key/value cache: argument checks, workspace layout, launches.
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -124,12 +125,15 @@ TokenArgs token_args(const int64_t* start, const int32_t* n_new, int32_t Tq) {
 }
 
 int num_sms() {
+  static std::atomic<int> known[64];
   int dev = 0, n = 148;
-  cudaGetDevice(&dev);
+  if (cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 && known[dev].load(std::memory_order_relaxed) > 0)
+    return known[dev].load(std::memory_order_relaxed);
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
     cudaGetLastError();
-    n = 148;
+    return 148;
   }
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -933,12 +933,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
 template <int D, bool kPair, int kW>
 cudaError_t launch_tc_as(const PagedAttendArgs& a, cudaStream_t s) {
   auto kernel = paged_attend_tc_kernel<D, kPair, kW>;
-  // the warps' register split draws on what the block was launched with
-  cudaFuncAttributes attr;
-  cudaError_t e = cudaFuncGetAttributes(&attr, kernel);
-  if (e != cudaSuccess) return e;
-  if (attr.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
-  e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), TcShape<D>::kBytes);
+  // the warps' register split draws on what the block was launched with: looked at once
+  static const int regs = [&] {
+    cudaFuncAttributes attr;
+    return cudaFuncGetAttributes(&attr, kernel) == cudaSuccess ? attr.numRegs : 0;
+  }();
+  if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
+  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), TcShape<D>::kBytes);
   if (e == cudaSuccess) e = launch_kernel(kernel, dim3(a.ctas), dim3(kThreads), TcShape<D>::kBytes, s, 0, a);
   if (e == cudaSuccess)
     e = launch_combine<D>(a, CombineShape{kPair ? 256 : 128, kKeys, 1, kPair ? 1 : 2, kShift}, s);
