@@ -522,21 +522,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     };
 
     // Scores of a half tile that the row at position t does not see become -inf, in tensor memory, and NaN
-    // where the key's V row has a NaN code.  16 columns at a time: the loops stay small (see the top).
+    // where the key's V row has a NaN code; 16 columns at a time, those that need it.
     auto hide = [&](const TileMeta& meta, int half, uint32_t tile, uint32_t sb, int t) {
 #pragma unroll 1
       for (int u = 0; u < 4; ++u) {
-        float y[16];
-        uint32_t yw[16];
-        __syncwarp();
-        tmem_ld_32x32b_x16(sb + 16u * u, y);
-        tmem_wait_ld();
         const int su = 4 * half + u, p0 = meta.pos + 16 * su;
-        uint32_t m = bits_to(t - p0);
+        uint32_t m = bits_to(t - p0) & 0xFFFFu;
         if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
         if (t < 0 || !((meta.have >> su) & 1u)) m = 0u;
         const uint32_t nb = *reinterpret_cast<const uint32_t*>(nans + (tile & 1) * 32 + 4 * su);
         const uint32_t bad = ((nb & 15u) | ((nb >> 4) & 0xF0u) | ((nb >> 8) & 0xF00u) | ((nb >> 12) & 0xF000u)) & m;
+        if (__all_sync(0xffffffffu, m == 0xFFFFu && bad == 0u)) continue;
+        float y[16];
+        uint32_t yw[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) y[c] = 0.f;
+        if (__any_sync(0xffffffffu, m != 0u)) {
+          tmem_ld_32x32b_x16(sb + 16u * u, y);
+          tmem_wait_ld();
+        }
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
           const float v = (m >> c) & 1u ? y[c] : -INFINITY;

@@ -82,6 +82,9 @@ __device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int pe
     Seg s;
     seg_load(a, s, i, row_tile, tile, per);
     sum += s.units;
+    // segments without work: nothing to join (the others' entries are written by whoever begins them)
+    if (s.units == 0 && blockIdx.x == 0)
+      for (int h = 0; h < a.Hkv; ++h) a.info[i * a.Hkv + h] = make_int2(0, 0);
   }
   sum *= a.Hkv;
   int64_t inc = sum;
@@ -176,52 +179,57 @@ struct CombineShape {
   float shift;                                // O is scaled by 2^shift
 };
 
-// Joins the records of the segments that were cut: a block per segment and four rows.
+// Joins the records of the segments that were cut: blockIdx.x is the segment, and the blocks of y share its
+// rows, 1024 / D at a time.
 template <int D>
-__global__ void __launch_bounds__(D) paged_combine_kernel(const __grid_constant__ PagedAttendArgs a,
-                                                          const __grid_constant__ CombineShape cs) {
+__global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constant__ PagedAttendArgs a,
+                                                            const __grid_constant__ CombineShape cs) {
+  constexpr int kPass = 1024 / D;
   const int seg = blockIdx.x, rows = cs.rows;
+  const int2 who = a.info[seg];
+  if (who.x >= who.y) return;                                 // one CTA had all of it, or there was nothing
   Seg s;
   seg_load(a, s, seg / a.Hkv, rows, cs.tile, cs.per);
   s.h = seg % a.Hkv;
-  const int r = blockIdx.y * 4 + threadIdx.x / (D / 4), c = (threadIdx.x % (D / 4)) * 4;
-  const int R = s.rb * rows + r, j = R / a.G, gr = R - j * a.G;
-  if (s.units == 0 || j >= s.n) return;
-  const int2 who = a.info[seg];
-  if (who.x >= who.y) return;                                 // one CTA had all of it
   const size_t floats = record_floats(rows, D);
-  float W = kNone, Z = kNone;
+  const int c = (threadIdx.x % (D / 4)) * 4;
+  for (int r = blockIdx.y * kPass + threadIdx.x / (D / 4); r < rows; r += gridDim.y * kPass) {
+    const int R = s.rb * rows + r, j = R / a.G, gr = R - j * a.G;
+    if (j >= s.n) break;
+    float W = kNone, Z = kNone;
 #pragma unroll 4
-  for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
-    const int q = i / cs.groups, g = i - q * cs.groups;
-    const float* st = record_of(a, q, who.x, floats * cs.groups) + g * floats + (size_t)rows * D + r;
-    W = fmaxf(W, st[0]);
-    Z = fmaxf(Z, st[rows]);
-  }
-  float L = 0.f;
-  float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
+      const int q = i / cs.groups, g = i - q * cs.groups;
+      const float* st = record_of(a, q, who.x, floats * cs.groups) + g * floats + (size_t)rows * D + r;
+      W = fmaxf(W, st[0]);
+      Z = fmaxf(Z, st[rows]);
+    }
+    float L = 0.f;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
-    const int q = i / cs.groups, g = i - q * cs.groups;
-    const float* rec = record_of(a, q, who.x, floats * cs.groups) + g * floats;
-    const float* st = rec + (size_t)rows * D + r;
-    const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
-    const float f = exp2f(st[0] - W);
-    L += st[2 * rows] * exp2f(st[rows] - Z);
-    v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+    for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
+      const int q = i / cs.groups, g = i - q * cs.groups;
+      const float* rec = record_of(a, q, who.x, floats * cs.groups) + g * floats;
+      const float* st = rec + (size_t)rows * D + r;
+      const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
+      const float f = exp2f(st[0] - W);
+      L += st[2 * rows] * exp2f(st[rows] - Z);
+      v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+    }
+    const int head = s.h * a.G + gr;
+    if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
+    const float f = Z == kNone && !(L != L) ? 0.f : exp2f(W - Z - cs.shift) / L;
+    const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+    const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
+    store_act4(a.out + at * act_bytes(a.act_fmt), a.act_fmt, 0, out);
   }
-  const int head = s.h * a.G + gr;
-  if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
-  const float f = Z == kNone && !(L != L) ? 0.f : exp2f(W - Z - cs.shift) / L;
-  const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
-  const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
-  store_act4(a.out + at * act_bytes(a.act_fmt), a.act_fmt, 0, out);
 }
 
 template <int D>
 cudaError_t launch_combine(const PagedAttendArgs& a, const CombineShape& cs, cudaStream_t s) {
-  return launch_kernel(paged_combine_kernel<D>, dim3((unsigned)(a.T.B * a.rb_max * a.Hkv), cs.rows / 4), dim3(D), 0, s,
-                       0, a, cs);
+  const int passes = (cs.rows + 1024 / D - 1) / (1024 / D);
+  return launch_kernel(paged_combine_kernel<D>, dim3((unsigned)(a.T.B * a.rb_max * a.Hkv), passes > 8 ? passes / 2 : passes),
+                       dim3(256), 0, s, 0, a, cs);
 }
 
 }  // namespace
