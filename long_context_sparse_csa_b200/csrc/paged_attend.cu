@@ -120,7 +120,7 @@ struct Shape {
   static constexpr int kQBytes = kTerms * NT * kWords * 32 * 8;
   static constexpr int kMergeBytes = kBufs * kRows * D * 4;
   static constexpr int kFixed = kQBytes + kMergeBytes + kRows * 4 + 3 * kWarps * kRows * 4;
-  static constexpr int kFree = 227 * 1024 - 1024 - 512 - kFixed;
+  static constexpr int kFree = 227 * 1024 - 1024 - 1024 - kFixed;
   static constexpr int kFit = kFree / (kWarps * (kStageBytes + 2 * (int)sizeof(Meta) + 8));
   static constexpr int kStages = kFit < 6 ? kFit : 6;
   static_assert(kStages >= 2, "ring");
@@ -132,7 +132,7 @@ struct Shape {
   static constexpr size_t kOffMeta = kOffStat + 3 * kWarps * kRows * 4;
   static constexpr size_t kOffBar = (kOffMeta + (size_t)kWarps * kStages * 2 * sizeof(Meta) + 7) / 8 * 8;
   static constexpr size_t kOffScan = kOffBar + (size_t)kWarps * kStages * 8;
-  static constexpr size_t kBytes = 1024 + kOffScan + kWarps * 8;
+  static constexpr size_t kBytes = 1024 + kOffScan + kScanWords * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -159,7 +159,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
     for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 3);  // one arrival with the bytes, two of the scales
     fence_barrier_init();
   }
-  const Run run = find_run(a, kRows, kTile, kWarps, reinterpret_cast<int64_t*>(sm + S::kOffScan));
+  const Run run = find_run(a, kRows, kTile, kWarps, 1, reinterpret_cast<int64_t*>(sm + S::kOffScan));
   if (run.u0 >= run.u1) return;
   const int steps = (int)(run.u1 - run.u0);
 

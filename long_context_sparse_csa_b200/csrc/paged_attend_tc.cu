@@ -9,11 +9,12 @@
 // Mathematics.  S = q K^T and O += P V with M = 128 query rows, f16 operands (e4m3 codes are exact in
 // f16; queries scaled per row by a power of two), f32 sums in tensor memory; P stays in tensor memory,
 // over S's columns, as the A operand of the second product.  Scales and the two running maxima as in
-// the warp-level kernel: O sums 2^(z + v - mw + 7) codes, z the logit in log2 units and v the log2 of the
+// the warp-level kernel: O sums 2^(z + v - mw + 4) codes, z the logit in log2 units and v the log2 of the
 // page's value scale; the denominator sums 2^(z - mz).  One exponential serves both: per 16 keys of a
-// page the weights' sum times 2^(mw - mz - v - 7), unless that factor is beyond 2^80 (pages' scales
+// page the weights' sum times 2^(mw - mz - v - 4), unless that factor is beyond 2^80 (pages' scales
 // very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when
-// some keys exceed it by more than 8 (then O is rescaled in tensor memory), so P stays up to 2^15.
+// some keys exceed it by more than 11 (then O is rescaled in tensor memory), so P stays up to 2^15 and keeps its
+// 11 bits down to 2^-18 of the largest weight (2^-29 of it below that, rounded either way).
 //
 // Roles (640 threads): warp 0 issues q K^T, warp 2 P V; warp 1 looks up the tiles' pages and scales; warps 4-7 and 8-11 are the two groups' softmax, a
 // thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles: 16-byte loads of codes, one tile ahead in
@@ -37,8 +38,8 @@ constexpr int kKeys = 128;
 constexpr int kThreads = 640;
 constexpr int kSubs = kKeys / 16;
 constexpr int kMeta = 8;                        // tiles looked up ahead, four at a time
-constexpr float kShift = 7.f;
-constexpr int kRegsLaunch = 96, kRegsSoftmax = 136, kRegsConvert = 72, kRegsIssue = 64;
+constexpr float kShift = 4.f;                   // P = 2^(weight + kShift), at most 2^15: a margin of 11
+constexpr int kRegsLaunch = 96, kRegsSoftmax = 128, kRegsConvert = 72, kRegsIssue = 80;
 static_assert(256 * kRegsSoftmax + 256 * kRegsConvert + 128 * kRegsIssue <= kThreads * kRegsLaunch, "register split");
 
 struct __align__(8) TcBars {
@@ -65,6 +66,7 @@ struct __align__(16) TileMeta {
 struct Part {
   Seg s;
   int sb, unit0, tiles;                       // first tile, number of tiles
+  uint32_t tile0;                             // tiles of the CTA's run before it
   bool complete;
 };
 
@@ -74,12 +76,9 @@ struct Parts {
   int64_t left;
 };
 
-// A warp's place in its CTA's run, in shared memory: the roles need it rarely and their registers more.
-struct WarpWalk {
-  Parts parts;
-  Part next, cur;
-  int more;
-};
+// Parts that the looking-up warp has published.  It is at most kMeta tiles ahead of the softmax, and the softmax
+// holds the part that it ends, so that twice as many entries need no waits of their own.
+constexpr int kParts = 2 * kMeta;
 
 template <int D>
 struct TcShape {
@@ -91,9 +90,9 @@ struct TcShape {
   static constexpr size_t kOffNan = kOffCq + 2 * 128 * 4;     // [2 stages][32] NaN flags of V's rows, four to a byte
   static constexpr size_t kOffBars = kOffNan + 64;
   static constexpr size_t kOffScan = kOffBars + (sizeof(TcBars) + 7) / 8 * 8;
-  static constexpr size_t kOffMeta = (kOffScan + (kThreads / 32) * 8 + 15) / 16 * 16;
-  static constexpr size_t kOffWalk = kOffMeta + kMeta * sizeof(TileMeta);
-  static constexpr size_t kBytes = 1024 + kOffWalk + (kThreads / 32) * sizeof(WarpWalk);
+  static constexpr size_t kOffMeta = (kOffScan + kScanWords * 8 + 15) / 16 * 16;
+  static constexpr size_t kOffParts = kOffMeta + kMeta * sizeof(TileMeta);
+  static constexpr size_t kBytes = 1024 + kOffParts + kParts * sizeof(Part);
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -276,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     }
     fence_barrier_init();
   }
-  const Run run = find_run(a, kRowTile, kKeys, 1, reinterpret_cast<int64_t*>(sm + S::kOffScan));
+  const Run run = find_run(a, kRowTile, kKeys, 1, 4, reinterpret_cast<int64_t*>(sm + S::kOffScan));
   if (run.u0 >= run.u1) return;
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -288,15 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
   const uint32_t tmem = bars->tmem_base;
   TileMeta* metas = reinterpret_cast<TileMeta*>(sm + S::kOffMeta);
   const int64_t run_tiles = run.u1 - run.u0;
-  WarpWalk& walk = reinterpret_cast<WarpWalk*>(sm + S::kOffWalk)[warp];
-  Part& pt = walk.next;
-  if (lane == 0) parts_start(a, walk.parts, run, kRowTile);
-  auto next_part = [&]() {
-    __syncwarp();
-    if (lane == 0) walk.more = parts_next(a, walk.parts, walk.next, kRowTile);
-    __syncwarp();
-    return walk.more != 0;
-  };
+  Part* part_ring = reinterpret_cast<Part*>(sm + S::kOffParts);
 
   if (warp < 4) {
     // ------------------------------------------------------------------ the products
@@ -404,13 +395,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     } else if (warp == 1) {
       // ---------------------------------------------------------------- pages and scales, four tiles at a time
       bool ok = true;
-      int i = 0, tmin = 0, tmax = 0;
-      bool more = next_part();
-      if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
+      int i = 0, tmin = 0, tmax = 0, parts_so_far = 0;
+      Parts walk;
+      Part pt;
+      parts_start(a, walk, run, kRowTile);
+      pt.tiles = 0;
+#pragma unroll 1
       for (int64_t n0 = 0; n0 < run_tiles; n0 += 4) {
         int pos = 0, h = 0, b = 0, limit = 0, index = 0;
         bool all = false;
-        for (int k = 0; k < 4 && n0 + k < run_tiles; ++k) {
+#pragma unroll 1
+        for (int k = 0; k < 4 && n0 + k < run_tiles; ++k, ++i) {
+          if (i == pt.tiles) {
+            i = 0;
+            parts_next(a, walk, pt, kRowTile);
+            row_span(a, pt.s, kRowTile, &tmin, &tmax);
+            pt.tile0 = (uint32_t)(n0 + k);
+            if (lane == 0) part_ring[parts_so_far % kParts] = pt;
+            ++parts_so_far;
+            __syncwarp();
+          }
           if ((lane >> 3) == k) {
             const int p0 = tile_pos(pt.s, pt.unit0 + i, kKeys);
             all = sees_all(a, p0, tmin, tmax);
@@ -420,13 +424,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             b = pt.s.b;
             limit = pt.s.start + pt.s.n;
           }
-          __syncwarp();
-          if (++i == pt.tiles) {
-            i = 0;
-            more = next_part();
-            if (more) row_span(a, pt.s, kRowTile, &tmin, &tmax);
-          }
         }
+        __syncwarp();
         const bool mine = n0 + (lane >> 3) < run_tiles;
         const int u = lane & 7, at = pos + 16 * u;
         int32_t pg = -1;
@@ -484,14 +483,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     auto load_q = [&](const Part& p) {
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
       const int c = lane % kLanes;
-#pragma unroll 4
+      // copied as they are, then scaled where they lie: short loops, as their code is run once a part
+#pragma unroll 1
       for (int it = 0; it < 32 / kPer; ++it) {
         const int r = 32 * w4 + it * kPer + lane / kLanes;
         const int R = p.s.rb * kRowTile + (kPair ? g * 128 : 0) + r, j = R / a.G, gr = R - j * a.G;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (j < p.s.n)
-          x = *reinterpret_cast<const uint4*>(
-              a.q + 2 * (((size_t)p.s.b * a.tok.Tq + j) * a.q_stride + (size_t)(p.s.h * a.G + gr) * D + 8 * c));
+        const bool live = j < p.s.n;
+        const uint8_t* from =
+            a.q + (live ? 2 * (((size_t)p.s.b * a.tok.Tq + j) * a.q_stride + (size_t)(p.s.h * a.G + gr) * D + 8 * c) : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                         smem_u32(Q + (c >> 3) * S::kHalf + sw128(r, c & 7))),
+                     "l"(from), "r"(live ? 16 : 0)
+                     : "memory");
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+      for (int it = 0; it < 32 / kPer; ++it) {
+        const int r = 32 * w4 + it * kPer + lane / kLanes;
+        uint4* at = reinterpret_cast<uint4*>(Q + (c >> 3) * S::kHalf + sw128(r, c & 7));
+        const uint4 x = *at;
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
         float f[8], am = 0.f;
 #pragma unroll
@@ -514,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         y.y = pack_f16x2(f[2] * up, f[3] * up);
         y.z = pack_f16x2(f[4] * up, f[5] * up);
         y.w = pack_f16x2(f[6] * up, f[7] * up);
-        *reinterpret_cast<uint4*>(Q + (c >> 3) * S::kHalf + sw128(r, c & 7)) = y;
+        *at = y;
       }
       fence_proxy_async_smem();
       __syncwarp();                                      // cqs: a warp's rows are its own
@@ -522,41 +532,40 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     };
 
     // Scores of a half tile that the row at position t does not see become -inf, in tensor memory, and NaN
-    // where the key's V row has a NaN code; 16 columns at a time, those that need it.
+    // where the key's V row has a NaN code.
     auto hide = [&](const TileMeta& meta, int half, uint32_t tile, uint32_t sb, int t) {
-#pragma unroll 1
+      uint32_t m[4], bad[4], rest = 0;
+#pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int su = 4 * half + u, p0 = meta.pos + 16 * su;
-        uint32_t m = bits_to(t - p0) & 0xFFFFu;
-        if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
-        if (t < 0 || !((meta.have >> su) & 1u)) m = 0u;
+        m[u] = bits_to(t - p0) & 0xFFFFu;
+        if (a.window > 0) m[u] &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
+        if (t < 0 || !((meta.have >> su) & 1u)) m[u] = 0u;
         const uint32_t nb = *reinterpret_cast<const uint32_t*>(nans + (tile & 1) * 32 + 4 * su);
-        const uint32_t bad = ((nb & 15u) | ((nb >> 4) & 0xF0u) | ((nb >> 8) & 0xF00u) | ((nb >> 12) & 0xF000u)) & m;
-        if (__all_sync(0xffffffffu, m == 0xFFFFu && bad == 0u)) continue;
-        float y[16];
-        uint32_t yw[16];
-#pragma unroll
-        for (int c = 0; c < 16; ++c) y[c] = 0.f;
-        if (__any_sync(0xffffffffu, m != 0u)) {
-          tmem_ld_32x32b_x16(sb + 16u * u, y);
-          tmem_wait_ld();
-        }
-#pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          const float v = (m >> c) & 1u ? y[c] : -INFINITY;
-          yw[c] = (bad >> c) & 1u ? 0x7fffffffu : __float_as_uint(v);
-        }
-        tmem_st_32x32b_x16(sb + 16u * u, yw);
+        bad[u] = ((nb & 15u) | ((nb >> 4) & 0xF0u) | ((nb >> 8) & 0xF00u) | ((nb >> 12) & 0xF000u)) & m[u];
+        rest |= (m[u] ^ 0xFFFFu) | bad[u];
       }
+      if (__all_sync(0xffffffffu, rest == 0u)) return;
+      float y[64];
+      tmem_ld_32x32b_x32(sb, y);
+      tmem_ld_32x32b_x32(sb + 32u, y + 32);
+      tmem_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 64; ++c) {
+        const float v = (m[c >> 4] >> (c & 15)) & 1u ? y[c] : -INFINITY;
+        y[c] = (bad[c >> 4] >> (c & 15)) & 1u ? __int_as_float(0x7fffffff) : v;
+      }
+      tmem_st_32x32b_x32(sb, y);
+      tmem_st_32x32b_x32(sb + 32u, y + 32);
       tmem_wait_st();
     };
 
     // Per part: its tiles; then the next part's queries, while the last product runs; then its end.
-    Part& cur = walk.cur;
+    int nparts = 0;                                      // parts so far
     float mw = kNone, mz = kNone, l = 0.f, cq = 0.f;
     int jobs = 0, j = 0, gr = 0, t = -1;
     // The end of the part `cur`: its answer, or its record.
-    auto finish = [&]() {
+    auto finish = [&](const Part& cur) {
       // ---------------------------------------------------------------- the part's end
       const int seg = cur.sb * a.Hkv + cur.s.h;
       if (g == 0 && row == 0 && cur.unit0 == 0) {
@@ -653,15 +662,17 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       return true;
     };
 
-    bool more = next_part(), any = false;
+    bool any = false;
+#pragma unroll 1
     for (;;) {
-      if (more && (kPair || pt.tiles > g)) load_q(pt);
-      if (any && !finish()) { ok = false; break; }
+      const bool more = tile0 < (uint32_t)run_tiles;
+      const Part& cur = part_ring[nparts % kParts];      // published with its first tile
+      if (more && !warp_wait(&bars->mfull[tile0 % kMeta], (tile0 / kMeta) & 1u)) { ok = false; break; }
+      if (more && (kPair || cur.tiles > g)) load_q(cur);
+      if (any && !finish(part_ring[(nparts - 1) % kParts])) { ok = false; break; }
       if (!more) break;
       any = true;
-      __syncwarp();
-      if (lane == 0) cur = pt;
-      __syncwarp();
+      ++nparts;
       jobs = kPair ? cur.tiles : (cur.tiles - g + 1) / 2;
       mw = mz = kNone;
       l = 0.f;
@@ -774,8 +785,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               cz = fmaxf(cz, zt);
               cw = fmaxf(cw, zt + meta.lv[u0 + u]);
             }
-            // a maximum moves where a key exceeds it by more than 8; the others' P fit as they are
-            const bool move = cw > mw + 8.f;
+            // a maximum moves where a key exceeds it by more than 11; the others' P fit as they are
+            const bool move = cw > mw + 11.f;
             const float nw = move ? cw : mw, nz = move ? fmaxf(mz, cz) : mz, al = ex2(mw - nw);
             l *= ex2(mz - nz);
             mw = nw;
@@ -817,7 +828,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       }
       tile0 += (uint32_t)cur.tiles;
       if (!ok) break;
-      more = next_part();
     }
     if (!ok) set_device_error(a.err, kErrWaitTimeout);
   } else {

@@ -73,60 +73,97 @@ struct Run {
   int sb, ctas;                               // CTAs with work: no more than units
 };
 
-__device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int64_t* scratch) {
+// Shared memory of find_run, in 8-byte words.
+constexpr int kScanWords = 100;
+
+// Runs are equal numbers of units, or, where that makes the longest run at most `slack` units longer, whole segments:
+// those leave no records to write and join.
+__device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int slack, int64_t* scratch) {
   const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
   const int n = a.T.B * a.rb_max;
   const int each = (n + nt - 1) / nt;
-  int64_t sum = 0;
+  int64_t sum = 0, cnt = 0;
+  int most = 0;
+#pragma unroll 1
   for (int i = tid * each; i < (tid + 1) * each && i < n; ++i) {
     Seg s;
     seg_load(a, s, i, row_tile, tile, per);
     sum += s.units;
+    cnt += s.units > 0;
+    most = s.units > most ? s.units : most;
     // segments without work: nothing to join (the others' entries are written by whoever begins them)
     if (s.units == 0 && blockIdx.x == 0)
       for (int h = 0; h < a.Hkv; ++h) a.info[i * a.Hkv + h] = make_int2(0, 0);
   }
   sum *= a.Hkv;
-  int64_t inc = sum;
+  cnt *= a.Hkv;
+  int64_t inc = sum, incc = cnt;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += up;
+    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o), upc = __shfl_up_sync(0xffffffffu, incc, o);
+    if (lane >= o) {
+      inc += up;
+      incc += upc;
+    }
   }
-  if (lane == 31) scratch[wid] = inc;
+  most = __reduce_max_sync(0xffffffffu, most);
+  if (lane == 31) {
+    scratch[wid] = inc;
+    scratch[32 + wid] = incc;
+    scratch[64 + wid] = most;
+  }
   __syncthreads();
-  int64_t base = 0, total = 0;
+  int64_t at = inc - sum, atc = incc - cnt, total = 0, segs = 0;
+#pragma unroll 1
   for (int w = 0; w < (nt >> 5); ++w) {
-    const int64_t v = scratch[w];
-    if (w < wid) base += v;
+    const int64_t v = scratch[w], vc = scratch[32 + w];
+    if (w < wid) {
+      at += v;
+      atc += vc;
+    }
     total += v;
+    segs += vc;
+    most = (int)scratch[64 + w] > most ? (int)scratch[64 + w] : most;
   }
-  __syncthreads();
   Run r;
   r.total = total;
-  r.ctas = total < a.ctas ? (int)total : a.ctas;
   r.u0 = r.u1 = 0;
-  if ((int)blockIdx.x < r.ctas) {
-    r.u0 = total * blockIdx.x / r.ctas;
-    r.u1 = total * (blockIdx.x + 1) / r.ctas;
-  }
-  int64_t at = base + inc - sum;
-  if (r.u0 < r.u1 && r.u0 >= at && r.u0 < at + sum) {
+  r.before = 0;
+  r.sb = 0;
+  const bool whole = (segs + a.ctas - 1) / a.ctas * most <= (total + a.ctas - 1) / a.ctas + slack;
+  const int64_t things = whole ? segs : total;
+  r.ctas = things < a.ctas ? (int)things : a.ctas;
+  if ((int)blockIdx.x >= r.ctas) return r;                    // the whole CTA
+  const int64_t t0 = things * blockIdx.x / r.ctas, t1 = things * (blockIdx.x + 1) / r.ctas;
+  // the threads whose (sequence, block)s hold the two ends
+  const int64_t mine = whole ? atc : at, count = whole ? cnt : sum;
+#pragma unroll 1
+  for (int end = 0; end < 2; ++end) {
+    const int64_t t = end ? t1 : t0;
+    if (t < mine || t >= mine + count) continue;
+    int64_t u = at, k = mine;                                 // units and things before (sequence, block) i
+#pragma unroll 1
     for (int i = tid * each;; ++i) {
       Seg s;
       seg_load(a, s, i, row_tile, tile, per);
-      const int64_t u = (int64_t)s.units * a.Hkv;
-      if (r.u0 < at + u) {
-        scratch[0] = i;
-        scratch[1] = at;
+      const int64_t units = (int64_t)s.units * a.Hkv, ks = whole ? (s.units > 0 ? a.Hkv : 0) : units;
+      if (t < k + ks) {
+        scratch[96 + 2 * end] = whole ? u + (t - k) * s.units : t;
+        if (end == 0) {
+          scratch[97] = u;
+          scratch[99] = i;
+        }
         break;
       }
-      at += u;
+      u += units;
+      k += ks;
     }
   }
   __syncthreads();
-  r.sb = (int)scratch[0];
-  r.before = scratch[1];
+  r.u0 = scratch[96];
+  r.u1 = t1 == things ? total : scratch[98];
+  r.before = scratch[97];
+  r.sb = (int)scratch[99];
   __syncthreads();
   return r;
 }
@@ -167,12 +204,8 @@ __device__ __forceinline__ int tile_pos(const Seg& s, int i, int tile) {
 // Floats of one partial record: O [rows][D], then mw, mz, l per row.
 __host__ __device__ constexpr size_t record_floats(int rows, int D) { return (size_t)rows * (D + 3); }
 
-// Record of CTA q's part of a segment that CTA `first` begins: a CTA's first segment may have begun
-// before it (record 0), its last may end after it (record 1); a segment that begins in it is record 1.
-__device__ __forceinline__ const float* record_of(const PagedAttendArgs& a, int q, int first, size_t floats) {
-  return a.part + ((size_t)q * 2 + (q == first ? 1 : 0)) * floats;
-}
-
+// Record `slot` of CTA q: its first segment may have begun before it (slot 0), its last may end after it
+// (slot 1); a segment that begins in it is slot 1.
 struct CombineShape {
   int rows, tile, per;                        // rows of a block, keys of a tile, tiles of a unit
   int groups;                                 // records of a part
@@ -196,25 +229,25 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   for (int r = blockIdx.y * kPass + threadIdx.x / (D / 4); r < rows; r += gridDim.y * kPass) {
     const int R = s.rb * rows + r, j = R / a.G, gr = R - j * a.G;
     if (j >= s.n) break;
-    float W = kNone, Z = kNone;
-#pragma unroll 4
-    for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
-      const int q = i / cs.groups, g = i - q * cs.groups;
-      const float* st = record_of(a, q, who.x, floats * cs.groups) + g * floats + (size_t)rows * D + r;
-      W = fmaxf(W, st[0]);
-      Z = fmaxf(Z, st[rows]);
-    }
-    float L = 0.f;
+    // records first .. last of the segment, `groups` to a CTA; CTA who.x's are its second ones
+    const float* first = a.part + ((size_t)who.x * 2 + 1) * cs.groups * floats + r;
+    const float* rest = a.part + (size_t)(who.x + 1) * 2 * cs.groups * floats + r;
+    float W = kNone, Z = kNone, L = 0.f;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = who.x * cs.groups; i < (who.y + 1) * cs.groups; ++i) {
-      const int q = i / cs.groups, g = i - q * cs.groups;
-      const float* rec = record_of(a, q, who.x, floats * cs.groups) + g * floats;
-      const float* st = rec + (size_t)rows * D + r;
-      const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
-      const float f = exp2f(st[0] - W);
-      L += st[2 * rows] * exp2f(st[rows] - Z);
-      v.x += x.x * f; v.y += x.y * f; v.z += x.z * f; v.w += x.w * f;
+    auto add = [&](const float* rec) {
+      const float4 x = *reinterpret_cast<const float4*>(rec + (size_t)r * (D - 1) + c);
+      const float w = rec[(size_t)rows * D], z = rec[(size_t)rows * (D + 1)], l = rec[(size_t)rows * (D + 2)];
+      const float nw = fmaxf(W, w), nz = fmaxf(Z, z), f = exp2f(W - nw), f1 = exp2f(w - nw);
+      L = L * exp2f(Z - nz) + l * exp2f(z - nz);
+      v.x = v.x * f + x.x * f1; v.y = v.y * f + x.y * f1; v.z = v.z * f + x.z * f1; v.w = v.w * f + x.w * f1;
+      W = nw;
+      Z = nz;
+    };
+#pragma unroll 1
+    for (int g = 0; g < cs.groups; ++g) {
+      add(first + g * floats);
+#pragma unroll 2
+      for (int q = 0; q < who.y - who.x; ++q) add(rest + ((size_t)q * 2 * cs.groups + g) * floats);
     }
     const int head = s.h * a.G + gr;
     if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
