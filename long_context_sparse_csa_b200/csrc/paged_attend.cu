@@ -110,8 +110,10 @@ template <int D, int NT, bool F32>
 struct Shape {
   static constexpr int kRows = 8 * NT;
   static constexpr int kTerms = F32 ? 3 : 1;
-  // Warps and merge buffers: as many as registers (O takes D/16 x NT x 4 of them) and shared memory allow.
-  static constexpr int kWarps = F32 || NT * D > 256 ? 8 : 12;
+  // Warps and merge buffers: as many as registers (O takes D/16 x NT x 4 of them) and shared memory allow.  1 M keys
+  // of 8 heads with 12 warps 387 us, with 8 447 us; 524,288 keys and 16 rows of 128 dims with 8 251 us, with 12
+  // (which spill) 473 us.
+  static constexpr int kWarps = F32 || NT * D > 128 ? 8 : 12;
   static constexpr int kBufs = NT * D > 128 ? 2 : 4;
   static constexpr int kThreads = 32 * kWarps;
   static constexpr bool kQRegs = NT == 1 && !F32;             // query fragments stay in registers
@@ -328,9 +330,9 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
       // S^T, scaled: z = logit (log2 units)
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
-        float acc[F32 ? 2 : 1][NT][4];
+        float acc[2][NT][4];                                  // two chains: even and odd words, or the large and small terms
 #pragma unroll
-        for (int c = 0; c < (F32 ? 2 : 1); ++c)
+        for (int c = 0; c < 2; ++c)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -358,7 +360,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
 #pragma unroll
             for (int c = kTerms - 1; c >= 0; --c) {           // the small terms apart from the large one
               const uint2 b = S::kQRegs ? qr[S::kQRegs ? w : 0] : qf[((c * NT + n) * kWords + w) * 32 + lane];
-              mma_f16(acc[F32 && c > 0 ? 1 : 0][n], fr, b.x, b.y);
+              mma_f16(acc[F32 ? (c > 0) : (w & 1)][n], fr, b.x, b.y);
             }
           }
         }
@@ -370,9 +372,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
           const float f0 = fminf(ks * c2.x, 3.0e38f), f1 = fminf(ks * c2.y, 3.0e38f);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            float v = acc[0][n][e];
-            if (F32) v += acc[F32 ? 1 : 0][n][e];
-            z[s][n][e] = v * ((e & 1) ? f1 : f0);
+            z[s][n][e] = (acc[0][n][e] + acc[1][n][e]) * ((e & 1) ? f1 : f0);
           }
         }
       }
