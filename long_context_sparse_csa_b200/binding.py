@@ -208,7 +208,9 @@ def _tensor(t, name, dtypes, shape):
 
 def _one_device(*tensors):
     d = tensors[0].get_device()
-    if any(t.get_device() != d for t in tensors):
+    for t in tensors:
+        if t.get_device() == d:
+            continue
         raise CsaError(1, "tensors on different devices: " + ", ".join(str(t.device) for t in tensors))
     return d
 
@@ -228,9 +230,11 @@ def make_page_pool(k, v, k_scale, v_scale) -> CsaPagePool:
 
 def make_page_table(table, refs, page) -> CsaPageTable:
     """Page table struct over table [B, table_cap] and refs [n_pages] (int32).  It keeps the tensors alive."""
-    _tensor(table, "table", (torch.int32,), (None, None))
-    _tensor(refs, "refs", (torch.int32,), (None,))
-    t = CsaPageTable(table.data_ptr(), refs.data_ptr(), table.shape[1], refs.shape[0], table.shape[0], page)
+    if not (table.dtype is refs.dtype is torch.int32 and table.dim() == 2 and refs.dim() == 1 and table.is_contiguous()
+            and refs.is_contiguous()):
+        raise CsaError(1, "table [B, table_cap] and refs [n_pages] must be contiguous torch.int32")
+    B, cap = table.shape
+    t = CsaPageTable(table.data_ptr(), refs.data_ptr(), cap, refs.numel(), B, page)
     t.keep, t.device = (table, refs), _one_device(table, refs)
     return t
 
@@ -427,7 +431,7 @@ _ACT = {0: torch.float32, 1: torch.bfloat16}
 def _here(T):
     """The device of the table's tensors, which has to be the current one (a kernel elsewhere could not read them)."""
     d = T.device
-    if d < 0 or d != torch.cuda.current_device():
+    if d < 0 or d != torch._C._cuda_getDevice():
         raise CsaError(1, f"the page table is on device {d} (-1: the CPU), not on the current device")
     return d
 

@@ -38,12 +38,21 @@ __device__ __forceinline__ void release_page(int32_t* ref, int* err) {
 // ----------------------------------------------------------------------------- append
 // One CTA per (sequence, page that the call writes, KV head, keys or values): the largest finite new
 // value, the page's scale, the new codes, and the earlier tokens' codes once more if the scale grew.
-// Each thread holds its part of the page (NV vectors of 8 values) in registers between the two passes,
-// so the new values are read once; earlier codes are read only where the scale grows.  A decode step
-// (one token) is bound by latency: table, count, values and scale are loaded before the first barrier.
-__device__ __forceinline__ void load8(const uint8_t* p, int fmt, float v[8]) {
-  load_act4(p, fmt, 0, v);
-  load_act4(p + 4 * act_bytes(fmt), fmt, 0, v + 4);
+// Each thread holds its part of the page (NV vectors of 8 values, as they came) in registers between the
+// two passes, so the new values are read once; earlier codes are read only where the scale grows.  A
+// decode step (one token) is bound by latency: the values are loaded beside the page's look-up.
+template <int FMT>
+__device__ __forceinline__ void unpack8(const uint4* raw, float v[8]) {
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(raw);
+#pragma unroll
+  for (int i = 0; i < (FMT == CSA_FMT_F32 ? 8 : 4); ++i) {
+    if (FMT == CSA_FMT_F32) {
+      v[i] = __uint_as_float(w[i]);
+    } else {
+      v[2 * i] = bf16_bits_to_f(w[i] & 0xFFFFu);
+      v[2 * i + 1] = bf16_bits_to_f(w[i] >> 16);
+    }
+  }
 }
 
 __device__ __forceinline__ uint2 encode8(const float v[8], float f) {
@@ -58,7 +67,7 @@ __device__ __forceinline__ uint2 encode8(const float v[8], float f) {
 }
 
 template <int FMT, int NV>
-__global__ void paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+__global__ void __launch_bounds__(256, FMT == CSA_FMT_F32 ? 2 : 4) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   __shared__ float scratch[32];
   uint32_t id = blockIdx.x;
   const int kv = id & 1;
@@ -74,43 +83,43 @@ __global__ void paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   if (off64 + n <= 0) return;
   const int off = (int)off64;
   const int64_t p = (start >> a.T.page_log2) + i;
-  if (p >= a.T.cap) {
-    if (threadIdx.x == 0) set_device_error(a.err, kErrPage);
-    return;
-  }
-  const int32_t g = a.T.table[(size_t)b * a.T.cap + p];
-  if (g < 0 || g >= a.T.n_pages || (a.T.refs && a.T.refs[g] > 1)) {
-    if (threadIdx.x == 0) set_device_error(a.err, kErrPage);
-    return;
-  }
   const int lo = off > 0 ? off : 0, hi = off + n < page ? off + n : page;
   const int tid = threadIdx.x, nt = blockDim.x;
   const int lane8 = a.D >> 3, dlog = a.D == 128 ? 4 : 3;
+  // the new values are on their way before the page is looked up: they do not depend on it
+  constexpr int kRaw = FMT == CSA_FMT_F32 ? 2 : 1;
   const uint8_t* src = (kv ? a.v_new : a.k_new);
+  uint4 raw[NV][kRaw];
+#pragma unroll
+  for (int u = 0; u < NV; ++u) {
+    const int e = u * nt + tid, slot = e >> dlog, c = (e & (lane8 - 1)) * 8;
+    const size_t at = ((size_t)b * a.tok.Tq + (slot - off)) * a.kv_stride + (size_t)h * a.D + c;
+#pragma unroll
+    for (int w = 0; w < kRaw; ++w)
+      raw[u][w] = slot >= lo && slot < hi ? __ldg(reinterpret_cast<const uint4*>(src + at * (FMT == CSA_FMT_F32 ? 4 : 2)) + w)
+                                          : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int32_t g = -1;
+  if (p < a.T.cap) g = a.T.table[(size_t)b * a.T.cap + p];
+  if (g < 0 || g >= a.T.n_pages || (a.T.refs && a.T.refs[g] > 1)) {
+    if (tid == 0) set_device_error(a.err, kErrPage);
+    return;
+  }
   const size_t gh = (size_t)g * a.Hkv + h;
   float* scale_p = (kv ? a.P.vs : a.P.ks) + gh;
   uint8_t* codes = (kv ? a.P.v : a.P.k) + gh * page * a.D;
   const float old = lo > 0 ? *scale_p : 0.f;
-  float x[NV][8];
   float amax = 0.f;
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
-    const int e = u * nt + tid, slot = e >> dlog, c = (e & (lane8 - 1)) * 8;
-    if (slot >= lo && slot < hi) {
-      const size_t at = ((size_t)b * a.tok.Tq + (slot - off)) * a.kv_stride + (size_t)h * a.D + c;
-      load8(src + at * (FMT == CSA_FMT_F32 ? 4 : 2), FMT, x[u]);
-    } else {
-#pragma unroll
-      for (int w = 0; w < 8; ++w) x[u][w] = 0.f;
-    }
-  }
-#pragma unroll
-  for (int u = 0; u < NV; ++u)
+    float x[8];
+    unpack8<FMT>(raw[u], x);
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
-      const float ax = fabsf(x[u][w]);
+      const float ax = fabsf(x[w]);
       if (ax < INFINITY) amax = fmaxf(amax, ax);
     }
+  }
   amax = block_max(amax, scratch);
   // the smallest power of two s >= 2^-126 with amax / s <= 448 = 0.875 * 2^9
   int ex = -126;
@@ -139,7 +148,11 @@ __global__ void paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
 #pragma unroll
   for (int u = 0; u < NV; ++u) {
     const int e = u * nt + tid, slot = e >> dlog;
-    if (slot >= lo && slot < hi) *reinterpret_cast<uint2*>(codes + (size_t)e * 8) = encode8(x[u], inv);
+    if (slot >= lo && slot < hi) {
+      float x[8];
+      unpack8<FMT>(raw[u], x);
+      *reinterpret_cast<uint2*>(codes + (size_t)e * 8) = encode8(x, inv);
+    }
   }
   if (tid == 0 && now != old) *scale_p = now;        // every thread read it before the reduction's barriers
 }
