@@ -210,7 +210,9 @@ csa_status_t csa_paged_attend(const csa_gqa_t* L, const csa_page_pool_t* pool, c
   a.P = pool_args(pool);
   a.tok = token_args(start, n_new, Tq);
   a.H = L->H; a.Hkv = L->Hkv; a.G = L->H / L->Hkv; a.D = L->D; a.act_fmt = L->act_format;
-  a.window = L->window; a.first = L->first;
+  // no position is n_max or more: a longer window shows the same keys, and keeps the kernels' sums within int32
+  a.window = L->window < n_max ? L->window : (int)n_max;
+  a.first = L->first;
   a.scale_log2 = (L->softmax_scale > 0 ? L->softmax_scale : 1.0f / sqrtf((float)L->D)) * kLog2e;
   a.n_max = (int)n_max;
   a.q = static_cast<const uint8_t*>(q);

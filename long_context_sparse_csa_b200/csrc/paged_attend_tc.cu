@@ -185,6 +185,10 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
+}
+
 // A whole warp's look at a barrier, and its bounded wait: true for all its lanes or for none.
 __device__ __forceinline__ bool warp_try(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     mbar_init(&bars->recfree, 128);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(&bars->mfull[i], kSubs);
-      mbar_init(&bars->mfree[i], 10 + (kPair ? 8 : 4));   // a lane of every warp that reads the entry
+      mbar_init(&bars->mfree[i], 18);                    // the 10 warps that copy and issue, 8 of the softmax (see below)
     }
     fence_barrier_init();
   }
@@ -673,6 +677,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       if (!more) break;
       any = true;
       ++nparts;
+      // Eight softmax warps let go of every tile's entry, so that neither group falls a ring behind the other: both
+      // groups' where both work on it, else the group's own warps twice; of a part's only tile, again both groups'.
+      const uint32_t shares = kPair || cur.tiles == 1 ? 1u : 2u;
+      if (!kPair && g == 1 && cur.tiles == 1 && lane == 0) mbar_arrive(&bars->mfree[tile0 % kMeta]);
       jobs = kPair ? cur.tiles : (cur.tiles - g + 1) / 2;
       mw = mz = kNone;
       l = 0.f;
@@ -681,6 +689,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       gr = R - j * a.G;
       t = j < cur.s.n ? cur.s.start + j : -1;
       cq = cqs[g * 128 + row];
+      // a warp without live rows only keeps the barriers going: what it leaves in its rows of P stays in theirs of O
+      const bool idle = __all_sync(0xffffffffu, j >= cur.s.n);
       // A half tile a step, in a short loop without rare cases: a wait that has to be waited for, keys that some row
       // does not see, P out of its range and scales far apart leave the loop, are dealt with below it, and
       // the step is taken up again.  (With those cases inside, the loop ran a quarter slower.)
@@ -704,8 +714,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             if ((c & 1) == 0 && !warp_try(&bars->mfull[tile % kMeta], (tile / kMeta) & 1u)) { why = kNoMeta; break; }
             if (!warp_try(&bars->sfull[g][buf], (job >> 1) & 1u)) { why = kNoScores; break; }
             tc_fence_after();
-            if (!meta.whole) { why = kHidden; break; }
+            if (!meta.whole && !idle) { why = kHidden; break; }
           }
+          if (!idle) {
           float x[64], fs[kU], ls[kU], sums[kU];         // scores; logit factor, log2 of the value scale, sum per kW keys
           uint32_t p[32];
           __syncwarp();
@@ -750,9 +761,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           tmem_st_32x32b_x16(sb, p);
           tmem_st_32x32b_x16(sb + 16u, p + 16);
           tmem_wait_st();
+          }
           tc_fence_before();
           mbar_arrive(&bars->pfull[g][buf]);
-          if ((c & 1) && lane == 0) mbar_arrive(&bars->mfree[tile % kMeta]);
+          if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
           seen = again = false;
           ++job;
           ++c;

@@ -307,6 +307,28 @@ def test_strided_queries_and_other_scale():
     _close(h(out), ref, _tolerance("bf16", ref, w, z))
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq,H", [(1, 4), (40, 8), (150, 2)])
+@pytest.mark.parametrize("window,first", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1), (1, 0), (1, 1)])
+def test_windows_and_first_tokens_at_the_ends_of_their_range(act, Tq, H, window, first):
+    rng = np.random.default_rng(16)
+    cache = Cache(rng, 30, 1, 16, 64)
+    table, _ = _table(rng, 2, 15, 30, [15, 15])
+    _close(*_attend(cache, table, [240 - Tq, 3], [Tq, Tq // 2 + 1], Tq, H, act, window, first, rng=rng))
+
+
+@pytest.mark.parametrize("Tq,H,Hkv", [(17, 1, 1), (40, 3, 1), (100, 4, 2), (33, 9, 1)])
+def test_row_blocks_with_few_rows_in_them(Tq, H, Hkv):
+    """Query rows that leave warps of a 128- or 256-row block without any."""
+    rng = np.random.default_rng(17)
+    lens = [70, 300, 129, 1025]
+    held = [-(-n // 32) for n in lens]
+    cache = Cache(rng, sum(held), Hkv, 32, 128)
+    table, _ = _table(rng, 4, max(held), cache.N, held)
+    n_new = [min(n, Tq) for n in lens]
+    _close(*_attend(cache, table, np.array(lens) - n_new, n_new, Tq, H, rng=rng))
+
+
 def test_long_sequences_split_over_the_gpu():
     """Hundreds of CTAs share a segment; the oracle is taken over a few heads of the same keys."""
     rng = np.random.default_rng(15)
