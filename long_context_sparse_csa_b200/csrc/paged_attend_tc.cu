@@ -189,6 +189,10 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(n) : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // A whole warp's look at a barrier, and its bounded wait: true for all its lanes or for none.
 __device__ __forceinline__ bool warp_try(uint64_t* bar, uint32_t parity) {
   return __all_sync(0xffffffffu, mbar_try_wait(bar, parity));
@@ -444,6 +448,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           const size_t gh = (size_t)pg * a.Hkv + h;
           ks = a.P.ks[gh];
           vs = a.P.vs[gh];
+          // the codes on their way to L2: the converting warps hold one tile ahead, too little for the latency of
+          // memory where few rows leave little else to do (4 tokens over 524,288 keys: 404 -> 393 us)
+          const size_t code = (gh * a.T.page + (at & (a.T.page - 1))) * D;
+          prefetch_l2(a.P.k + code, 16 * D);
+          prefetch_l2(a.P.v + code, 16 * D);
         }
         const uint32_t have = (__ballot_sync(0xffffffffu, pg >= 0) >> (lane & 24)) & 0xFFu;
         const float lv = (float)((int)((__float_as_uint(vs) >> 23) & 255u) - 127);
