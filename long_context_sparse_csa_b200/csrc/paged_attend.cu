@@ -4,6 +4,9 @@
 // What bounds it.  A decode step reads 2 D bytes per key and KV head and does 4 D G flops with them
 // (G query heads of the group): at G = 8 that is 16 flops a byte, so memory bounds it.  The design
 // keeps bytes in flight: 8 or 12 warps per SM, each with its own ring of 32-key tiles that TMA fills.
+// Measured, 64 heads on 8 KV heads of 128 dims: 1,048,576 keys in 361-379 us (5.7-5.9 TB/s, 0.86-0.91 of the
+// measured copy rate), 8 sequences of up to 131,072 in 268-276 us; about 640 instructions per tile and warp,
+// half of them code conversions and byte permutes, leave little of the clock unused.
 //
 // Work.  A segment is one (sequence, block of query rows, KV head); a row is (token, head of the
 // group).  Its visible keys are cut into tiles of 32 (positions in multiples of 32; with a window, the

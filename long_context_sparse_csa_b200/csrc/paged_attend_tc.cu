@@ -4,7 +4,10 @@
 // What bounds it.  With hundreds of rows per KV head the products are 4 D flops per (row, key): the
 // tensor core, and beside it the exponentials (one per 4 D = 512 flops at D = 128: at 16 a clock the
 // same 2,048 clocks per 256 x 128 tile that the products take).  Two groups of 128 rows work in turns:
-// while one group's softmax runs, the tensor core works for the other.
+// while one group's softmax runs, the tensor core works for the other.  Measured, 2,048 tokens of 64 heads of
+// 128 dims behind 14,336: 1,245 us, 828 TFLOP/s (half of the bf16 peak), 5,000 clocks a tile; the tensor
+// pipe is active 40 % of the time, the exponential unit 34 %, issue slots 42 %: no unit is full, the softmax
+// warps' latencies and the half tiles' products (96 KB of shared memory reads each) add up.
 //
 // Mathematics.  S = q K^T and O += P V with M = 128 query rows, f16 operands (e4m3 codes are exact in
 // f16; queries scaled per row by a power of two), f32 sums in tensor memory; P stays in tensor memory,
@@ -16,12 +19,12 @@
 // some keys exceed it by more than 11 (then O is rescaled in tensor memory), so P stays up to 2^15 and keeps its
 // 11 bits down to 2^-18 of the largest weight (2^-29 of it below that, rounded either way).
 //
-// Roles (640 threads): warp 0 issues q K^T, warp 2 P V; warp 1 looks up the tiles' pages and scales; warps 4-7 and 8-11 are the two groups' softmax, a
-// thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles: 16-byte loads of codes, one tile ahead in
-// registers, to f16 in the 128-byte swizzle (two stages each).  A job is one (tile, group).  With more
-// than 128 rows (kPair) the groups take different rows of the same tile; otherwise the same rows of
+// Roles (640 threads): warp 0 issues q K^T, warp 2 P V; warp 1 looks up the tiles' pages and scales; warps 4-7
+// and 8-11 are the two groups' softmax, a thread a row; warps 12-15 convert K tiles, warps 16-19 V tiles:
+// 16-byte loads of codes, one tile ahead in registers, to f16 in the 128-byte swizzle (two stages each).
+// With more than 128 rows (kPair) the groups take different rows of the same tile; otherwise the same rows of
 // alternate tiles, joined at the end.  A group works through half tiles in two buffers of S: while it
-// weighs one, the other's scores are computed.  P lies over its S, so the next S there waits for the product
+// weighs one, the other's scores are computed (one buffer of whole tiles: 1,460 us against 1,434).  P lies over its S, so the next S there waits for the product
 // that reads it.
 #include <cuda_fp16.h>
 
