@@ -70,7 +70,8 @@ __device__ __forceinline__ uint2 encode8(const float v[8], float f) {
 }
 
 template <int FMT, int NV>
-__global__ void __launch_bounds__(256, FMT == CSA_FMT_F32 ? 2 : 4) paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
+__global__ void __launch_bounds__(256, FMT == CSA_FMT_F32 ? 2 : 4)
+paged_append_kernel(const __grid_constant__ PagedAppendArgs a) {
   __shared__ float scratch[32];
   uint32_t id = blockIdx.x;
   const int kv = id & 1;

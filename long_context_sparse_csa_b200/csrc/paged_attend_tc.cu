@@ -24,8 +24,8 @@
 // 16-byte loads of codes, one tile ahead in registers, to f16 in the 128-byte swizzle (two stages each).
 // With more than 128 rows (kPair) the groups take different rows of the same tile; otherwise the same rows of
 // alternate tiles, joined at the end.  A group works through half tiles in two buffers of S: while it
-// weighs one, the other's scores are computed (one buffer of whole tiles: 1,460 us against 1,434).  P lies over its S, so the next S there waits for the product
-// that reads it.
+// weighs one, the other's scores are computed (one buffer of whole tiles: 1,460 us against 1,434).  P lies
+// over its S, so the next S there waits for the product that reads it.
 #include <cuda_fp16.h>
 
 #include "paged_walk.cuh"
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     const uint32_t s_addr = lane_addr + (uint32_t)(g * 128), o_addr = lane_addr + 256u + (uint32_t)(g * D);
     uint8_t* Q = sm + (size_t)g * S::kTileBytes;
     bool ok = true;
-    uint32_t job = 0, tile0 = 0, shared = 0;            // half tiles of this group, tiles of the CTA, segments shared by the groups
+    uint32_t job = 0, tile0 = 0, shared = 0;            // this group's half tiles, the CTA's tiles, segments the groups share
 
     // The group's queries: D / 8 lanes a row, scaled by a power of two to at most 2^15, as f16.
     auto load_q = [&](const Part& p) {
