@@ -27,6 +27,7 @@
 // weighs one, the other's scores are computed (one buffer of whole tiles: 1,460 us against 1,434).  P lies
 // over its S, so the next S there waits for the product that reads it.
 #include <cuda_fp16.h>
+#include <type_traits>
 
 #include "paged_walk.cuh"
 #include "sm100.cuh"
@@ -51,6 +52,7 @@ struct __align__(8) TcBars {
   uint64_t sfull[2][2], pfull[2][2], pvdone[2][2];      // [group][S buffer]
   uint64_t recfull, recfree;
   uint64_t mfull[kMeta], mfree[kMeta];
+  uint64_t part0;                             // the first part is published (the others with their first tiles)
   uint32_t tmem_base;
 };
 
@@ -280,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     }
     mbar_init(&bars->recfull, 128);
     mbar_init(&bars->recfree, 128);
+    mbar_init(&bars->part0, 1);
     for (int i = 0; i < kMeta; ++i) {
       mbar_init(&bars->mfull[i], kSubs);
       mbar_init(&bars->mfree[i], 18);                    // the 10 warps that copy and issue, 8 of the softmax (see below)
@@ -422,7 +425,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             parts_next(a, walk, pt, kRowTile);
             row_span(a, pt.s, kRowTile, &tmin, &tmax);
             pt.tile0 = (uint32_t)(n0 + k);
-            if (lane == 0) part_ring[parts_so_far % kParts] = pt;
+            if (lane == 0) {
+              part_ring[parts_so_far % kParts] = pt;
+              if (parts_so_far == 0) mbar_arrive(&bars->part0);
+            }
             ++parts_so_far;
             __syncwarp();
           }
@@ -500,10 +506,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       constexpr int kLanes = D / 8, kPer = 32 / kLanes;
       const int c = lane % kLanes;
       // copied as they are, then scaled where they lie: short loops, as their code is run once a part
+      int r = 32 * w4 + lane / kLanes;
+      const int R = p.s.rb * kRowTile + (kPair ? g * 128 : 0) + r;
+      int j = R / a.G, gr = R - j * a.G;
 #pragma unroll 1
       for (int it = 0; it < 32 / kPer; ++it) {
-        const int r = 32 * w4 + it * kPer + lane / kLanes;
-        const int R = p.s.rb * kRowTile + (kPair ? g * 128 : 0) + r, j = R / a.G, gr = R - j * a.G;
         const bool live = j < p.s.n;
         const uint8_t* from =
             a.q + (live ? 2 * (((size_t)p.s.b * a.tok.Tq + j) * a.q_stride + (size_t)(p.s.h * a.G + gr) * D + 8 * c) : 0);
@@ -511,11 +518,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
                          smem_u32(Q + (c >> 3) * S::kHalf + sw128(r, c & 7))),
                      "l"(from), "r"(live ? 16 : 0)
                      : "memory");
+        r += kPer;
+        for (gr += kPer; gr >= a.G; gr -= a.G) ++j;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 1
+#pragma unroll 2
       for (int it = 0; it < 32 / kPer; ++it) {
-        const int r = 32 * w4 + it * kPer + lane / kLanes;
+        r = 32 * w4 + it * kPer + lane / kLanes;
         uint4* at = reinterpret_cast<uint4*>(Q + (c >> 3) * S::kHalf + sw128(r, c & 7));
         const uint4 x = *at;
         const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
@@ -547,33 +556,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       mbar_arrive(&bars->qfull[g]);
     };
 
-    // Scores of a half tile that the row at position t does not see become -inf, in tensor memory, and NaN
-    // where the key's V row has a NaN code.
-    auto hide = [&](const TileMeta& meta, int half, uint32_t tile, uint32_t sb, int t) {
-      uint32_t m[4], bad[4], rest = 0;
+    // Scores x of a half tile that the row at position t does not see become -inf, and NaN where the key's V row
+    // has a NaN code.
+    auto mask = [&](const TileMeta& meta, int half, uint32_t tile, int t, float* x) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         const int su = 4 * half + u, p0 = meta.pos + 16 * su;
-        m[u] = bits_to(t - p0) & 0xFFFFu;
-        if (a.window > 0) m[u] &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
-        if (t < 0 || !((meta.have >> su) & 1u)) m[u] = 0u;
+        uint32_t m = bits_to(t - p0);
+        if (a.window > 0) m &= ~bits_to(t - a.window - p0) | bits_to(a.first - 1 - p0);
+        if (t < 0 || !((meta.have >> su) & 1u)) m = 0u;
         const uint32_t nb = *reinterpret_cast<const uint32_t*>(nans + (tile & 1) * 32 + 4 * su);
-        bad[u] = ((nb & 15u) | ((nb >> 4) & 0xF0u) | ((nb >> 8) & 0xF00u) | ((nb >> 12) & 0xF000u)) & m[u];
-        rest |= (m[u] ^ 0xFFFFu) | bad[u];
-      }
-      if (__all_sync(0xffffffffu, rest == 0u)) return;
-      float y[64];
-      tmem_ld_32x32b_x32(sb, y);
-      tmem_ld_32x32b_x32(sb + 32u, y + 32);
-      tmem_wait_ld();
 #pragma unroll
-      for (int c = 0; c < 64; ++c) {
-        const float v = (m[c >> 4] >> (c & 15)) & 1u ? y[c] : -INFINITY;
-        y[c] = (bad[c >> 4] >> (c & 15)) & 1u ? __int_as_float(0x7fffffff) : v;
+        for (int c = 0; c < 16; ++c) x[16 * u + c] = (m >> c) & 1u ? x[16 * u + c] : -INFINITY;
+        if (__builtin_expect(nb != 0u, 0)) {
+          const uint32_t bad = ((nb & 15u) | ((nb >> 4) & 0xF0u) | ((nb >> 8) & 0xF00u) | ((nb >> 12) & 0xF000u)) & m;
+#pragma unroll
+          for (int c = 0; c < 16; ++c) x[16 * u + c] = (bad >> c) & 1u ? __int_as_float(0x7fffffff) : x[16 * u + c];
+        }
       }
-      tmem_st_32x32b_x32(sb, y);
-      tmem_st_32x32b_x32(sb + 32u, y + 32);
-      tmem_wait_st();
     };
 
     // Per part: its tiles; then the next part's queries, while the last product runs; then its end.
@@ -683,7 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     for (;;) {
       const bool more = tile0 < (uint32_t)run_tiles;
       const Part& cur = part_ring[nparts % kParts];      // published with its first tile
-      if (more && !warp_wait(&bars->mfull[tile0 % kMeta], (tile0 / kMeta) & 1u)) { ok = false; break; }
+      if (more && !(nparts == 0 ? warp_wait(&bars->part0, 0u) : warp_wait(&bars->mfull[tile0 % kMeta], (tile0 / kMeta) & 1u))) {
+        ok = false;
+        break;
+      }
       if (more && (kPair || cur.tiles > g)) load_q(cur);
       if (any && !finish(part_ring[(nparts - 1) % kParts])) { ok = false; break; }
       if (!more) break;
@@ -713,9 +716,58 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       const int steps = 2 * jobs;
       int c = 0;
       bool seen = false, again = false;                  // the half tile's scores are there; its range has been seen to
+      bool over = false;
+      // The step's P over its scores, and its share of the denominator; true (and nothing done) where P leaves its range.
+      auto step = [&](auto masked, uint32_t tile, uint32_t sb, const TileMeta& meta) {
+        float x[64], fs[kU], ls[kU], sums[kU];         // scores; logit factor, log2 of the value scale, sum per kW keys
+        uint32_t p[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(sb, x);
+        tmem_ld_32x32b_x32(sb + 32u, x + 32);
+        const int u0 = 4 * (c & 1);
+#pragma unroll
+        for (int v = 0; v < kU; ++v) {
+          fs[v] = fmaxf(fminf(meta.ks[u0 + v * (kW / 16)] * cq, 3.0e38f), 1.2e-38f);
+          ls[v] = meta.lv[u0 + v * (kW / 16)];
+        }
+        const float back0 = mw - mz - kShift;
+        const bool far = back0 - meta.lv_min[c & 1] > 80.f;
+        tmem_wait_ld();
+        if (decltype(masked)::value) mask(meta, c & 1, tile, t, x);
+        over = false;
+#pragma unroll
+        for (int v = 0; v < kU; ++v) {
+          const float* xs = x + kW * v;
+          const float b = ls[v] - mw + kShift;
+          float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+          const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
+#pragma unroll
+          for (int q = 0; q < kW; q += 4) {
+            float2 y0 = fma2(make_float2(xs[q], xs[q + 1]), f2, b2);
+            float2 y1 = fma2(make_float2(xs[q + 2], xs[q + 3]), f2, b2);
+            y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
+            s0 = add2(s0, y0);
+            s1 = add2(s1, y1);
+            p[(kW * v + q) / 2] = pack_f16x2(y0.x, y0.y);
+            p[(kW * v + q) / 2 + 1] = pack_f16x2(y1.x, y1.y);
+          }
+          s0 = add2(s0, s1);
+          sums[v] = s0.x + s0.y;
+          over |= sums[v] > 60000.f;
+        }
+        if (__any_sync(0xffffffffu, over || far) && !again) return true;
+#pragma unroll
+        for (int v = 0; v < kU; ++v) {
+          const float back = back0 - ls[v];
+          if (!(back > 80.f)) l = fmaf(sums[v], ex2(back), l);
+        }
+        tmem_st_32x32b_x16(sb, p);
+        tmem_st_32x32b_x16(sb + 16u, p + 16);
+        tmem_wait_st();
+        return false;
+      };
       for (;;) {
         enum { kDone, kNoMeta, kNoScores, kHidden, kRange } why;
-        bool over;
 #pragma unroll 1
         for (;;) {
           if (c == steps) { why = kDone; break; }
@@ -728,52 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             tc_fence_after();
             if (!meta.whole && !idle) { why = kHidden; break; }
           }
-          if (!idle) {
-          float x[64], fs[kU], ls[kU], sums[kU];         // scores; logit factor, log2 of the value scale, sum per kW keys
-          uint32_t p[32];
-          __syncwarp();
-          tmem_ld_32x32b_x32(sb, x);
-          tmem_ld_32x32b_x32(sb + 32u, x + 32);
-          const int u0 = 4 * (c & 1);
-#pragma unroll
-          for (int v = 0; v < kU; ++v) {
-            fs[v] = fmaxf(fminf(meta.ks[u0 + v * (kW / 16)] * cq, 3.0e38f), 1.2e-38f);
-            ls[v] = meta.lv[u0 + v * (kW / 16)];
-          }
-          const float back0 = mw - mz - kShift;
-          const bool far = back0 - meta.lv_min[c & 1] > 80.f;
-          tmem_wait_ld();
-          over = false;
-#pragma unroll
-          for (int v = 0; v < kU; ++v) {
-            const float* xs = x + kW * v;
-            const float b = ls[v] - mw + kShift;
-            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            const float2 f2 = make_float2(fs[v], fs[v]), b2 = make_float2(b, b);
-#pragma unroll
-            for (int q = 0; q < kW; q += 4) {
-              float2 y0 = fma2(make_float2(xs[q], xs[q + 1]), f2, b2);
-              float2 y1 = fma2(make_float2(xs[q + 2], xs[q + 3]), f2, b2);
-              y0.x = ex2(y0.x); y0.y = ex2(y0.y); y1.x = ex2(y1.x); y1.y = ex2(y1.y);
-              s0 = add2(s0, y0);
-              s1 = add2(s1, y1);
-              p[(kW * v + q) / 2] = pack_f16x2(y0.x, y0.y);
-              p[(kW * v + q) / 2 + 1] = pack_f16x2(y1.x, y1.y);
-            }
-            s0 = add2(s0, s1);
-            sums[v] = s0.x + s0.y;
-            over |= sums[v] > 60000.f;
-          }
-          if (__any_sync(0xffffffffu, over || far) && !again) { why = kRange; break; }
-#pragma unroll
-          for (int v = 0; v < kU; ++v) {
-            const float back = back0 - ls[v];
-            if (!(back > 80.f)) l = fmaf(sums[v], ex2(back), l);
-          }
-          tmem_st_32x32b_x16(sb, p);
-          tmem_st_32x32b_x16(sb + 16u, p + 16);
-          tmem_wait_st();
-          }
+          if (!idle && step(std::false_type(), tile, sb, meta)) { why = kRange; break; }
           tc_fence_before();
           mbar_arrive(&bars->pfull[g][buf]);
           if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
@@ -791,9 +798,26 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           ok = warp_wait(&bars->sfull[g][buf], (job >> 1) & 1u);
         } else if (why == kHidden) {
           ok = warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u);            // the NaN flags
-          if (ok) hide(meta, c & 1, tile, sb, t);
-          seen = true;
-        } else {
+          if (!ok) break;
+          if (!step(std::true_type(), tile, sb, meta)) {
+            tc_fence_before();
+            mbar_arrive(&bars->pfull[g][buf]);
+            if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
+            ++job;
+            ++c;
+            continue;
+          }
+          float x[64];                                   // out of range: the masked scores stay, and the maxima move
+          tmem_ld_32x32b_x32(sb, x);
+          tmem_ld_32x32b_x32(sb + 32u, x + 32);
+          tmem_wait_ld();
+          mask(meta, c & 1, tile, t, x);
+          tmem_st_32x32b_x32(sb, x);
+          tmem_st_32x32b_x32(sb + 32u, x + 32);
+          tmem_wait_st();
+          why = kRange;
+        }
+        if (why == kRange) {
           const int u0 = 4 * (c & 1);
           if (__any_sync(0xffffffffu, over)) {
             float cz = -INFINITY, cw = -INFINITY;

@@ -130,11 +130,16 @@ __device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int pe
   r.u0 = r.u1 = 0;
   r.before = 0;
   r.sb = 0;
-  const bool whole = (segs + a.ctas - 1) / a.ctas * most <= (total + a.ctas - 1) / a.ctas + slack;
+  const int64_t share = total / a.ctas;                       // units of a CTA, rounded down
+  const bool whole = (int64_t)(((uint32_t)segs + a.ctas - 1) / a.ctas) * most <= share + (total > share * a.ctas) + slack;
   const int64_t things = whole ? segs : total;
   r.ctas = things < a.ctas ? (int)things : a.ctas;
   if ((int)blockIdx.x >= r.ctas) return r;                    // the whole CTA
-  const int64_t t0 = things * blockIdx.x / r.ctas, t1 = things * (blockIdx.x + 1) / r.ctas;
+  // things * c / ctas, without a wide division
+  const int64_t each_q = whole ? (int64_t)((uint32_t)segs / (uint32_t)r.ctas) : (total < a.ctas ? 1 : share);
+  const uint32_t each_r = (uint32_t)(things - each_q * r.ctas);
+  const int64_t t0 = each_q * blockIdx.x + each_r * blockIdx.x / (uint32_t)r.ctas;
+  const int64_t t1 = each_q * (blockIdx.x + 1) + each_r * (blockIdx.x + 1) / (uint32_t)r.ctas;
   // the threads whose (sequence, block)s hold the two ends
   const int64_t mine = whole ? atc : at, count = whole ? cnt : sum;
 #pragma unroll 1
