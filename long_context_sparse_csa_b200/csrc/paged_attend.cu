@@ -136,8 +136,7 @@ struct Shape {
   static constexpr size_t kOffStat = kOffCq + kRows * 4;      // [3][warps][rows]: mw, mz, l
   static constexpr size_t kOffMeta = kOffStat + 3 * kWarps * kRows * 4;
   static constexpr size_t kOffBar = (kOffMeta + (size_t)kWarps * kStages * 2 * sizeof(Meta) + 7) / 8 * 8;
-  static constexpr size_t kOffScan = kOffBar + (size_t)kWarps * kStages * 8;
-  static constexpr size_t kBytes = 1024 + kOffScan + kScanWords * 8;
+  static constexpr size_t kBytes = 1024 + kOffBar + (size_t)kWarps * kStages * 8;
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
@@ -164,7 +163,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
     for (int i = 0; i < kStages; ++i) mbar_init(&bars[i], 3);  // one arrival with the bytes, two of the scales
     fence_barrier_init();
   }
-  const Run run = find_run(a, kRows, kTile, kWarps, 1, reinterpret_cast<int64_t*>(sm + S::kOffScan));
+  const Run run = find_run(a, kRows, kTile, kWarps, 1);
   if (run.u0 >= run.u1) return;
   const int steps = (int)(run.u1 - run.u0);
 

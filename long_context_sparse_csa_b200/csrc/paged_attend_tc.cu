@@ -94,8 +94,7 @@ struct TcShape {
   static constexpr size_t kOffCq = 6 * (size_t)kTileBytes;    // [2][128] logit factor of a row
   static constexpr size_t kOffNan = kOffCq + 2 * 128 * 4;     // [2 stages][32] NaN flags of V's rows, four to a byte
   static constexpr size_t kOffBars = kOffNan + 64;
-  static constexpr size_t kOffScan = kOffBars + (sizeof(TcBars) + 7) / 8 * 8;
-  static constexpr size_t kOffMeta = (kOffScan + kScanWords * 8 + 15) / 16 * 16;
+  static constexpr size_t kOffMeta = (kOffBars + sizeof(TcBars) + 15) / 16 * 16;
   static constexpr size_t kOffParts = kOffMeta + kMeta * sizeof(TileMeta);
   static constexpr size_t kBytes = 1024 + kOffParts + kParts * sizeof(Part);
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     }
     fence_barrier_init();
   }
-  const Run run = find_run(a, kRowTile, kKeys, 1, 4, reinterpret_cast<int64_t*>(sm + S::kOffScan));
+  const Run run = find_run(a, kRowTile, kKeys, 1, 4);
   if (run.u0 >= run.u1) return;
   if (warp == 0) {
     tmem_alloc(&bars->tmem_base, 512);
@@ -522,7 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         for (gr += kPer; gr >= a.G; gr -= a.G) ++j;
       }
       asm volatile("cp.async.wait_all;" ::: "memory");
-#pragma unroll 2
+#pragma unroll 4
       for (int it = 0; it < 32 / kPer; ++it) {
         r = 32 * w4 + it * kPer + lane / kLanes;
         uint4* at = reinterpret_cast<uint4*>(Q + (c >> 3) * S::kHalf + sw128(r, c & 7));
@@ -780,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             tc_fence_after();
             if (!meta.whole && !idle) { why = kHidden; break; }
           }
-          if (!idle && step(std::false_type(), tile, sb, meta)) { why = kRange; break; }
+          if (!idle && ((c == 0 && !again) || step(std::false_type(), tile, sb, meta))) { why = kRange; break; }
           tc_fence_before();
           mbar_arrive(&bars->pfull[g][buf]);
           if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
@@ -799,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         } else if (why == kHidden) {
           ok = warp_wait(&bars->vfull[tile & 1], (tile >> 1) & 1u);            // the NaN flags
           if (!ok) break;
-          if (!step(std::true_type(), tile, sb, meta)) {
+          if (c > 0 && !step(std::true_type(), tile, sb, meta)) {
             tc_fence_before();
             mbar_arrive(&bars->pfull[g][buf]);
             if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
@@ -819,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         }
         if (why == kRange) {
           const int u0 = 4 * (c & 1);
-          if (__any_sync(0xffffffffu, over)) {
+          if (c == 0 || __any_sync(0xffffffffu, over)) {         // a part's first keys: no maxima yet
             float cz = -INFINITY, cw = -INFINITY;
 #pragma unroll 1
             for (int u = 0; u < 4; ++u) {

@@ -66,110 +66,106 @@ __device__ __forceinline__ void seg_load(const PagedAttendArgs& a, Seg& s, int s
   seg_range(a, s, row_tile, tile, per);
 }
 
-// This CTA's run of units [u0, u1) of all segments' units; *sb and *before: the (sequence, block) that
-// holds u0 and the units of the segments before it.  All threads of the CTA call it.
+// This CTA's run of units [u0, u1) of all segments' units, and where it begins.
 struct Run {
-  int64_t u0, u1, before, total;
-  int sb, ctas;                               // CTAs with work: no more than units
+  int64_t u0, u1, total;
+  int sb, h, unit;                            // (sequence, block), KV head and unit of the segment that hold u0
+  int ctas;                                   // CTAs with work: no more than units
 };
 
-// Shared memory of find_run, in 8-byte words.
-constexpr int kScanWords = 100;
-
 // Runs are equal numbers of units, or, where that makes the longest run at most `slack` units longer, whole segments:
-// those leave no records to write and join.
-__device__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int slack, int64_t* scratch) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, wid = tid >> 5;
+// those leave no records to write and join.  Every warp finds the run for itself (a lane takes every 32nd part of the
+// (sequence, block)s): with one scan over the whole CTA, its barriers and shared memory, this took 4 us of a
+// kernel's start.
+__device__ __forceinline__ Run find_run(const PagedAttendArgs& a, int row_tile, int tile, int per, int slack) {
+  const int lane = threadIdx.x & 31;
   const int n = a.T.B * a.rb_max;
-  const int each = (n + nt - 1) / nt;
-  int64_t sum = 0, cnt = 0;
-  int most = 0;
+  const int each = (n + 31) >> 5;
+  int64_t sum = 0;
+  int cnt = 0, most = 0;
 #pragma unroll 1
-  for (int i = tid * each; i < (tid + 1) * each && i < n; ++i) {
+  for (int i = lane * each; i < (lane + 1) * each && i < n; ++i) {
     Seg s;
     seg_load(a, s, i, row_tile, tile, per);
     sum += s.units;
     cnt += s.units > 0;
     most = s.units > most ? s.units : most;
     // segments without work: nothing to join (the others' entries are written by whoever begins them)
-    if (s.units == 0 && blockIdx.x == 0)
+    if (s.units == 0 && blockIdx.x == 0 && threadIdx.x < 32)
       for (int h = 0; h < a.Hkv; ++h) a.info[i * a.Hkv + h] = make_int2(0, 0);
   }
   sum *= a.Hkv;
   cnt *= a.Hkv;
-  int64_t inc = sum, incc = cnt;
+  int64_t at = sum;
+  int atc = cnt;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, inc, o), upc = __shfl_up_sync(0xffffffffu, incc, o);
+    const int64_t up = __shfl_up_sync(0xffffffffu, at, o);
+    const int upc = __shfl_up_sync(0xffffffffu, atc, o);
     if (lane >= o) {
-      inc += up;
-      incc += upc;
+      at += up;
+      atc += upc;
     }
-  }
-  most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 31) {
-    scratch[wid] = inc;
-    scratch[32 + wid] = incc;
-    scratch[64 + wid] = most;
-  }
-  __syncthreads();
-  int64_t at = inc - sum, atc = incc - cnt, total = 0, segs = 0;
-#pragma unroll 1
-  for (int w = 0; w < (nt >> 5); ++w) {
-    const int64_t v = scratch[w], vc = scratch[32 + w];
-    if (w < wid) {
-      at += v;
-      atc += vc;
-    }
-    total += v;
-    segs += vc;
-    most = (int)scratch[64 + w] > most ? (int)scratch[64 + w] : most;
   }
   Run r;
-  r.total = total;
+  r.total = __shfl_sync(0xffffffffu, at, 31);
+  const int segs = __shfl_sync(0xffffffffu, atc, 31);
+  most = __reduce_max_sync(0xffffffffu, most);
+  at -= sum;
+  atc -= cnt;
   r.u0 = r.u1 = 0;
-  r.before = 0;
-  r.sb = 0;
-  const int64_t share = total / a.ctas;                       // units of a CTA, rounded down
-  const bool whole = (int64_t)(((uint32_t)segs + a.ctas - 1) / a.ctas) * most <= share + (total > share * a.ctas) + slack;
-  const int64_t things = whole ? segs : total;
+  r.sb = r.h = r.unit = 0;
+  // units of a CTA, rounded down
+  const int64_t share = r.total >> 32 ? r.total / a.ctas : (int64_t)((uint32_t)r.total / (uint32_t)a.ctas);
+  const bool whole =
+      (int64_t)(((uint32_t)segs + a.ctas - 1) / a.ctas) * most <= share + (r.total > share * a.ctas) + slack;
+  const int64_t things = whole ? segs : r.total;
   r.ctas = things < a.ctas ? (int)things : a.ctas;
-  if ((int)blockIdx.x >= r.ctas) return r;                    // the whole CTA
+  if ((int)blockIdx.x >= r.ctas) return r;
   // things * c / ctas, without a wide division
-  const int64_t each_q = whole ? (int64_t)((uint32_t)segs / (uint32_t)r.ctas) : (total < a.ctas ? 1 : share);
+  const int64_t each_q = whole ? (int64_t)((uint32_t)segs / (uint32_t)r.ctas) : (r.total < a.ctas ? 1 : share);
   const uint32_t each_r = (uint32_t)(things - each_q * r.ctas);
-  const int64_t t0 = each_q * blockIdx.x + each_r * blockIdx.x / (uint32_t)r.ctas;
-  const int64_t t1 = each_q * (blockIdx.x + 1) + each_r * (blockIdx.x + 1) / (uint32_t)r.ctas;
-  // the threads whose (sequence, block)s hold the two ends
   const int64_t mine = whole ? atc : at, count = whole ? cnt : sum;
 #pragma unroll 1
   for (int end = 0; end < 2; ++end) {
-    const int64_t t = end ? t1 : t0;
-    if (t < mine || t >= mine + count) continue;
+    const int64_t t = each_q * (blockIdx.x + end) + each_r * (blockIdx.x + end) / (uint32_t)r.ctas;
+    if (t >= things) {                                        // only the last run's end
+      r.u1 = r.total;
+      break;
+    }
+    // the lane whose (sequence, block)s hold it
+    const bool here = t >= mine && t < mine + count;
     int64_t u = at, k = mine;                                 // units and things before (sequence, block) i
+    int i = lane * each, units = 0;
+    if (here) {
 #pragma unroll 1
-    for (int i = tid * each;; ++i) {
-      Seg s;
-      seg_load(a, s, i, row_tile, tile, per);
-      const int64_t units = (int64_t)s.units * a.Hkv, ks = whole ? (s.units > 0 ? a.Hkv : 0) : units;
-      if (t < k + ks) {
-        scratch[96 + 2 * end] = whole ? u + (t - k) * s.units : t;
-        if (end == 0) {
-          scratch[97] = u;
-          scratch[99] = i;
-        }
-        break;
+      for (;; ++i) {
+        Seg s;
+        seg_load(a, s, i, row_tile, tile, per);
+        units = s.units;
+        const int64_t us = (int64_t)units * a.Hkv, ks = whole ? (units > 0 ? a.Hkv : 0) : us;
+        if (t < k + ks) break;
+        u += us;
+        k += ks;
       }
-      u += units;
-      k += ks;
+    }
+    const int from = __ffs(__ballot_sync(0xffffffffu, here)) - 1;
+    i = __shfl_sync(0xffffffffu, i, from);
+    units = __shfl_sync(0xffffffffu, units, from);
+    u = __shfl_sync(0xffffffffu, u, from);
+    k = t - __shfl_sync(0xffffffffu, k, from);                // things into it
+    const int h = whole ? (int)k : (int)(k >> 32 ? k / units : (int64_t)((uint32_t)k / (uint32_t)units));
+    const int unit = whole ? 0 : (int)(k - (int64_t)h * units);
+    u += (int64_t)h * units + unit;
+    if (end == 0) {
+      r.u0 = u;
+      r.sb = i;
+      r.h = h;
+      r.unit = unit;
+    } else {
+      r.u1 = u;
     }
   }
-  __syncthreads();
-  r.u0 = scratch[96];
-  r.u1 = t1 == things ? total : scratch[98];
-  r.before = scratch[97];
-  r.sb = (int)scratch[99];
-  __syncthreads();
   return r;
 }
 
@@ -184,9 +180,8 @@ __device__ __forceinline__ void walk_start(const PagedAttendArgs& a, Walk& w, co
                                            int per) {
   w.sb = r.sb;
   seg_load(a, w.s, w.sb, row_tile, tile, per);
-  const int64_t in = r.u0 - r.before;
-  w.s.h = (int)(in / w.s.units);
-  w.unit = (int)(in - (int64_t)w.s.h * w.s.units);
+  w.s.h = r.h;
+  w.unit = r.unit;
 }
 
 __device__ __forceinline__ void walk_next(const PagedAttendArgs& a, Walk& w, int row_tile, int tile, int per) {
