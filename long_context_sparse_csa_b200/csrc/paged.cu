@@ -613,12 +613,12 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int o = (u * 256 + threadIdx.x) * 16;
-      if (o < bytes) x[u] = *reinterpret_cast<const uint4*>(from + o);
+      if (o < bytes) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + o));
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
       const int o = (u * 256 + threadIdx.x) * 16;
-      if (o < bytes) *reinterpret_cast<uint4*>(to + o) = x[u];
+      if (o < bytes) __stcs(reinterpret_cast<uint4*>(to + o), x[u]);
     }
     if (c == 0) {
       float* sc = kv ? a.P.vs : a.P.ks;

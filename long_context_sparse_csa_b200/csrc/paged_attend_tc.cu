@@ -926,24 +926,20 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         if (!warp_try(&freeb[tile & 1], ((tile >> 1) & 1u) ^ 1u)) { why = kNoRoom; break; }
         if (!clean) { why = kMasked; break; }
         uint8_t* dst = tiles + (tile & 1) * S::kTileBytes;
-#pragma unroll 1
-        for (int i0 = 0; i0 < kLoads; i0 += kLoads / 2) {
 #pragma unroll
-          for (int it = 0; it < kLoads / 2; ++it) {
-            const int r = (i0 + it) * 4 * kRowsPer + r0;
-            const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
-            uint4 y0, y1;
-            e4m3x4_f16(xw[0], y0.x, y0.y);
-            e4m3x4_f16(xw[1], y0.z, y0.w);
-            e4m3x4_f16(xw[2], y1.x, y1.y);
-            e4m3x4_f16(xw[3], y1.z, y1.w);
-            // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
-            uint8_t* at = dst + (c >> 2) * S::kHalf;
-            const int jx = (c & 3) * 2, up = (c >> 2) & 1;
-            *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
-            *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
-            x[it] = x[it + kLoads / 2];
-          }
+        for (int it = 0; it < kLoads; ++it) {
+          const int r = it * 4 * kRowsPer + r0;
+          const uint32_t xw[4] = {x[it].x, x[it].y, x[it].z, x[it].w};
+          uint4 y0, y1;
+          e4m3x4_f16(xw[0], y0.x, y0.y);
+          e4m3x4_f16(xw[1], y0.z, y0.w);
+          e4m3x4_f16(xw[2], y1.x, y1.y);
+          e4m3x4_f16(xw[3], y1.z, y1.w);
+          // the two 16-byte pieces, the second first in the upper half, so that a row's lanes fall on different banks
+          uint8_t* at = dst + (c >> 2) * S::kHalf;
+          const int jx = (c & 3) * 2, up = (c >> 2) & 1;
+          *reinterpret_cast<uint4*>(at + sw128(r, jx + up)) = up ? y1 : y0;
+          *reinterpret_cast<uint4*>(at + sw128(r, jx + (up ^ 1))) = up ? y0 : y1;
         }
         fence_proxy_async_smem();
         mbar_arrive(&full[tile & 1]);
