@@ -583,11 +583,14 @@ __global__ void pages_rewrite_kernel(const __grid_constant__ PagesCompactArgs a)
 }
 
 // ----------------------------------------------------------------------------- copy
-// Pieces of 16 KB of a page's keys or values, four 16-byte loads in flight per thread; the CTAs walk
-// the pieces of all pairs.
-constexpr int kPiece = 16384;
+// Pieces of 32 KB of a page's keys or values, eight 16-byte loads in flight per thread; the CTAs walk the pieces
+// of all pairs, the next piece's pages on their way while a piece is copied.  900 pages of 128 KB: 45 us (5.2
+// TB/s); with pieces of 16 KB 49 us, of 4 KB (16 CTAs per SM) 50.
+constexpr int kPiece = 32768;
+constexpr int kCopyThreads = 256;
+constexpr int kCopyLoads = kPiece / 16 / kCopyThreads;
 
-__global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__ PagesCopyArgs a) {
+__global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_constant__ PagesCopyArgs a) {
   int n = a.n;
   if (a.count) {
     const int c = *a.count;
@@ -595,34 +598,47 @@ __global__ void __launch_bounds__(256) pages_copy_kernel(const __grid_constant__
   }
   const int per = (int)((a.page_bytes + kPiece - 1) / kPiece);
   const int64_t items = (int64_t)n * 2 * per;
+  if (blockIdx.x >= items) return;
+  int i = (int)(blockIdx.x / (2 * per)), r = (int)(blockIdx.x - (int64_t)i * 2 * per);
+  const int step_i = (int)(gridDim.x / (2 * per)), step_r = (int)(gridDim.x - (int64_t)step_i * 2 * per);
+  int32_t s = a.src[i], d = a.dst[i];
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = (int)(it / (2 * per));
-    const int r = (int)(it - (int64_t)i * 2 * per);
     const int kv = r >= per, c = kv ? r - per : r;
-    const int32_t s = a.src[i], d = a.dst[i];
-    if (s < 0 || d < 0) continue;
-    if (s >= a.n_pages || d >= a.n_pages) {
+    const int32_t from_page = s, to_page = d;
+    i += step_i;
+    r += step_r;
+    if (r >= 2 * per) {
+      r -= 2 * per;
+      ++i;
+    }
+    if (it + gridDim.x < items) {
+      s = a.src[i];
+      d = a.dst[i];
+    }
+    if (from_page < 0 || to_page < 0) continue;
+    if (from_page >= a.n_pages || to_page >= a.n_pages) {
       if (threadIdx.x == 0) set_device_error(a.err, kErrPage);
       continue;
     }
     uint8_t* base = kv ? a.P.v : a.P.k;
-    const uint8_t* from = base + (size_t)s * a.page_bytes + (size_t)c * kPiece;
-    uint8_t* to = base + (size_t)d * a.page_bytes + (size_t)c * kPiece;
+    const uint8_t* from = base + (size_t)from_page * a.page_bytes + (size_t)c * kPiece;
+    uint8_t* to = base + (size_t)to_page * a.page_bytes + (size_t)c * kPiece;
     const int64_t bytes = a.page_bytes - (int64_t)c * kPiece;
-    uint4 x[4];
+    uint4 x[kCopyLoads];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int o = (u * 256 + threadIdx.x) * 16;
-      if (o < bytes) x[u] = __ldcs(reinterpret_cast<const uint4*>(from + o));
+    for (int u = 0; u < kCopyLoads; ++u) {
+      const int o = (u * kCopyThreads + threadIdx.x) * 16;
+      if (o < bytes) x[u] = *reinterpret_cast<const uint4*>(from + o);
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int o = (u * 256 + threadIdx.x) * 16;
-      if (o < bytes) __stcs(reinterpret_cast<uint4*>(to + o), x[u]);
+    for (int u = 0; u < kCopyLoads; ++u) {
+      const int o = (u * kCopyThreads + threadIdx.x) * 16;
+      if (o < bytes) *reinterpret_cast<uint4*>(to + o) = x[u];
     }
     if (c == 0) {
       float* sc = kv ? a.P.vs : a.P.ks;
-      for (int h = threadIdx.x; h < a.Hkv; h += 256) sc[(size_t)d * a.Hkv + h] = sc[(size_t)s * a.Hkv + h];
+      for (int h = threadIdx.x; h < a.Hkv; h += kCopyThreads)
+        sc[(size_t)to_page * a.Hkv + h] = sc[(size_t)from_page * a.Hkv + h];
     }
   }
 }
@@ -670,7 +686,8 @@ cudaError_t launch_pages_compact(const PagesCompactArgs& a, cudaStream_t s) {
 cudaError_t launch_pages_copy(const PagesCopyArgs& a, int num_sms, cudaStream_t s) {
   const int64_t items = (int64_t)a.n * 2 * ((a.page_bytes + kPiece - 1) / kPiece);
   const int64_t most = (int64_t)num_sms * 8;
-  return launch_kernel(pages_copy_kernel, dim3((unsigned)(items < most ? items : most)), dim3(256), 0, s, 0, a);
+  return launch_kernel(pages_copy_kernel, dim3((unsigned)(items < most ? items : most)), dim3(kCopyThreads),
+                       0, s, 0, a);
 }
 
 }  // namespace csa
