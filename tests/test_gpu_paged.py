@@ -764,6 +764,70 @@ def test_a_captured_step_follows_its_inputs():
     del graph
 
 
+def test_one_workspace_for_calls_of_different_shapes():
+    """Nothing that a call leaves in the workspace reaches the next one, whatever its shape and kernel."""
+    rng = np.random.default_rng(7)
+    Hkv, D, page, cap, B = 2, 64, 32, 70, 6
+    cache = Cache(rng, B * cap, Hkv, page, D)
+    table, _ = _table(rng, B, cap, cache.N, [cap] * B)
+    pool, td = cache.up(), _dev(table)
+    calls = []
+    for H, act, Tq, n in ((4, "bf16", 1, 6), (32, "bf16", 40, 6), (2, "f32", 3, 2), (2, "bf16", 300, 1), (16, "bf16", 5, 6),
+                          (4, "bf16", 2, 3), (2, "bf16", 700, 6)):
+        T = C.make_page_table(td[:n], _ints(cache.N, 0), page)
+        G = C.make_gqa(H, Hkv, D, act_format=act)
+        q = torch.randn(n, Tq, H, D, device="cuda").to(torch.float32 if act == "f32" else torch.bfloat16)
+        start = _dev(rng.integers(-1, cap * page - Tq, n))
+        n_new = _dev(rng.integers(0, Tq + 1, n).astype(np.int32))
+        calls.append((G, T, q, start, n_new, Tq))
+    size = max(C.csa_paged_workspace_size(c[0], c[1], c[5], cap * page) for c in calls)
+    shared = torch.zeros(size, dtype=torch.uint8, device="cuda")
+
+    def run(c, ws):
+        out = torch.zeros_like(c[2])
+        C.csa_paged_attend(c[0], pool, c[1], c[2], None, c[3], c[4], c[5], cap * page, out, ws)
+        return out
+
+    alone = [run(c, torch.zeros(size, dtype=torch.uint8, device="cuda")) for c in calls]
+    for i in rng.integers(0, len(calls), 60):
+        assert torch.equal(run(calls[i], shared), alone[i]), i
+    assert C.csa_device_error(shared) == 0
+
+
+def test_a_captured_chunk_follows_its_inputs():
+    """Prompt chunks of a padded batch in a graph, replayed beside an eager call on another stream."""
+    rng = np.random.default_rng(8)
+    B, Tq, H, Hkv, D, page, cap = 3, 70, 8, 2, 128, 16, 40
+    cache = Cache(rng, B * cap, Hkv, page, D)
+    table, _ = _table(rng, B, cap, cache.N, [cap] * B)
+    pool = cache.up()
+    T, G = C.make_page_table(_dev(table), _ints(cache.N, 0), page), C.make_gqa(H, Hkv, D, 200, 5)
+    q = torch.randn(B, Tq, H, D, device="cuda").bfloat16()
+    start, n_new = torch.zeros(B, dtype=torch.int64, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    size = C.csa_paged_workspace_size(G, T, Tq, cap * page)
+    ws, ws2 = (torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(2))
+    out, other = torch.zeros_like(q), torch.zeros_like(q)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    C.csa_paged_attend(G, pool, T, q, None, start, n_new, Tq, cap * page, out, ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        C.csa_paged_attend(G, pool, T, q, None, start, n_new, Tq, cap * page, out, ws)
+    h = lambda t: t.float().cpu().numpy().astype(np.float64)  # noqa: E731
+    for i in range(6):
+        start.copy_(_dev(rng.integers(-1, cap * page - Tq, B)))
+        n_new.copy_(_dev(rng.integers(0, Tq + 1, B).astype(np.int32)))
+        torch.cuda.synchronize()
+        graph.replay()
+        C.csa_paged_attend(G, pool, T, q, None, start, n_new, Tq, cap * page, other, ws2, stream=side)
+        torch.cuda.synchronize()
+        ref, asked, w, z = O.attend(cache.k, cache.v, cache.ks, cache.vs, table, page, h(q), start.cpu().numpy(),
+                                    n_new.cpu().numpy(), cap * page, 200, 5)
+        for o in (out, other):
+            _close(h(o)[asked], ref[asked], _tolerance("bf16", ref, w, z)[asked])
+    assert C.csa_device_error(ws) == 0 and C.csa_device_error(ws2) == 0
+    del graph
+
+
 def test_two_calls_at_once_on_two_streams():
     rng = np.random.default_rng(6)
     n, page = 4000, 32
