@@ -15,8 +15,9 @@
 // the warp-level kernel: O sums 2^(z + v - mw + 4) codes, z the logit in log2 units and v the log2 of the
 // page's value scale; the denominator sums 2^(z - mz).  One exponential serves both: per 16 keys of a
 // page the weights' sum times 2^(mw - mz - v - 4), unless that factor is beyond 2^80 (pages' scales
-// very far apart), where the denominators' exponentials are taken apart.  A maximum moves only when
-// some keys exceed it by more than 11 (then O is rescaled in tensor memory), so P stays up to 2^15 and keeps its
+// very far apart), where the denominators' exponentials are taken apart and the denominator's maximum follows
+// logits more than 40 above it.  O's maximum, and with it the other, moves only when some keys exceed it by
+// more than 11 (then O is rescaled in tensor memory), so P stays up to 2^15 and keeps its
 // 11 bits down to 2^-18 of the largest weight (2^-29 of it below that, rounded either way).
 //
 // Roles (640 threads): warp 0 issues q K^T, warp 2 P V; warp 1 looks up the tiles' pages and scales; warps 4-7
@@ -818,11 +819,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
         }
         if (why == kRange) {
           const int u0 = 4 * (c & 1);
-          if (c == 0 || __any_sync(0xffffffffu, over)) {         // a part's first keys: no maxima yet
+          const bool far = mw - mz - kShift - meta.lv_min[c & 1] > 80.f;
+          if (c == 0 || __any_sync(0xffffffffu, over || far)) {  // a part's first keys: no maxima yet
             float cz = -INFINITY, cw = -INFINITY;
 #pragma unroll 1
             for (int u = 0; u < 4; ++u) {
               float y[16];
+              __syncwarp();
               tmem_ld_32x32b_x16(sb + 16u * u, y);
               tmem_wait_ld();
               float m16 = y[0];
@@ -832,13 +835,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               cz = fmaxf(cz, zt);
               cw = fmaxf(cw, zt + meta.lv[u0 + u]);
             }
-            // a maximum moves where a key exceeds it by more than 11; the others' P fit as they are
+            // A maximum moves where a key exceeds it by more than 11; the others' P fit as they are.  The denominator's
+            // moves by itself where a key's logit exceeds it by more than 40 (its value's scale is as much smaller):
+            // the weights' sums then stay below 2^(80 + 16) a unit of keys, those taken apart below 2^40 a key.
             const bool move = cw > mw + 11.f;
-            const float nw = move ? cw : mw, nz = move ? fmaxf(mz, cz) : mz, al = ex2(mw - nw);
-            l *= ex2(mz - nz);
+            const float nw = move ? cw : mw, nz = move || cz > mz + 40.f ? fmaxf(mz, cz) : mz, al = ex2(mw - nw);
+            const float down = ex2(0.5f * (mz - nz));    // in two steps: l may be 2^100 where the factor is 2^-130
+            l = l * down * down;
             mw = nw;
             mz = nz;
-            if (c > 0) {                                 // O, once the group's last product is complete
+            if (c > 0 && __any_sync(0xffffffffu, move)) {        // O, once the group's last product is complete
               ok = warp_wait(&bars->pvdone[g][(job - 1) & 1u], ((job - 1) >> 1) & 1u);
               tc_fence_after();
 #pragma unroll 1

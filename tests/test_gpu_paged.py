@@ -259,6 +259,46 @@ def test_value_scales_far_apart(act, Tq, H):
     _close(*_attend(cache, table, [n - Tq], None, Tq, H, act, rng=rng, q=q))
 
 
+def _logit_pages(rng, page, D, logits, vscale, Hkv=1):
+    """A pool in table order whose page p holds keys of logit (log2 units) about logits[p] for the query (c, 0, ...)
+    of `_along`, and values of scale vscale[p]."""
+    N = len(logits)
+    cache = Cache(rng, N, Hkv, page, D)
+    cache.ks[:] = 2.0 ** -3
+    cache.k[:] = e4m3_encode(rng.integers(-1, 2, cache.k.shape) * 1.0)
+    for p, z in enumerate(logits):
+        cache.k[p, ..., 0] = e4m3_encode(np.full(cache.k[p, ..., 0].shape, np.round(z / 16) * 16.0))
+    cache.vs[:] = np.asarray(vscale, np.float64)[:, None].astype(np.float32)
+    return cache, np.arange(N, dtype=np.int32)[None]
+
+
+def _along(rng, Tq, H, D):
+    """Queries whose first channel turns a key's first code into as many log2 units (scale 2^-3, 1/sqrt(D))."""
+    q = rng.standard_normal((1, Tq, H, D)) * 0.25
+    q[..., 0] = 8 * np.sqrt(D) / np.log2(np.e)
+    return q
+
+
+@pytest.mark.parametrize("act,Tq,H", [("bf16", 1, 4), ("f32", 3, 4), ("bf16", 5, 4), ("bf16", 40, 8), ("bf16", 300, 1)])
+@pytest.mark.parametrize("order", [[0, 1], [1, 0], [0, 1, 2], [1, 2, 0], [2, 1, 0, 1], [2, 0, 2, 1, 2], [3, 1, 2], [2, 3, 2], [3, 2],
+                                   [2, 4, 5], [0, 4, 1], [4, 3, 5, 0]])
+@pytest.mark.parametrize("repeat", [24, 400])
+def test_large_logits_on_pages_of_small_values(act, Tq, H, order, repeat):
+    """The largest logits far above the others, on pages whose values are far below: the denominator's maximum has to
+    follow the logits although the weighted values' maximum stays.  24 pages are a few tiles, 400 are more than a
+    CTA's part."""
+    rng = np.random.default_rng(len(order) + repeat)
+    page, D = 16, 64
+    kinds = {0: (0, 2.0 ** 100), 1: (160, 2.0 ** -110), 2: (0, 2.0 ** -8), 3: (144, 2.0 ** -126), 4: (320, 2.0 ** -100),
+             5: (416, 2.0 ** -60)}
+    pages = [kinds[i] for i in order for _ in range(repeat // len(order))]
+    cache, table = _logit_pages(rng, page, D, [z for z, _ in pages], [s for _, s in pages])
+    zero = np.array([z == 144 for z, _ in pages])
+    cache.v[zero] = 0                                       # as an append of zeros leaves a page
+    n = len(pages) * page
+    _close(*_attend(cache, table, [n - Tq], None, Tq, H, act, rng=rng, q=_along(rng, Tq, H, D)))
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("Tq,H", [(1, 4), (40, 8)])
 def test_key_scales_and_queries_far_from_one(act, Tq, H):
