@@ -597,10 +597,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
       }
       if (complete) {
         const int head = cw.s.h * a.G + gr;
-        float den = L;
-        if (a.sinks) den += exp2f(a.sinks[head] * kLog2e - Z);
-        // O is relative to W (and 2^kShift), the denominator to Z
-        const float f = Z == kNone && L == 0.f ? 0.f : exp2f(W - Z - kShift) / den;
+        const float f = answer_factor(W, Z, L, a.sinks, head, kShift);
         const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
         const size_t at = (((size_t)cw.s.b * a.tok.Tq + j) * a.H + head) * D + c;
         store_act4(a.out + at * (F32 ? 4 : 2), F32 ? CSA_FMT_F32 : CSA_FMT_BF16, 0, out);

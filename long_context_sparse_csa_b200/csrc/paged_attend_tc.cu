@@ -618,9 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           den = l * exp2f(mz - Z) + other[(size_t)kRowTile * (D + 2) + rr] * exp2f(z1 - Z);
           f1 = exp2f(w1 - W);
         }
-        const bool none = Z == kNone && den == 0.f;
-        if (a.sinks) den += exp2f(a.sinks[head] * kLog2e - Z);
-        const float top = none ? 0.f : exp2f(W - Z - kShift) / den;
+        const float top = answer_factor(W, Z, den, a.sinks, head, kShift);
         f = exp2f(mw - W) * top;
         f1 *= top;
       }

@@ -201,6 +201,19 @@ __device__ __forceinline__ int tile_pos(const Seg& s, int i, int tile) {
   return (i < s.ta ? i : s.tb + (i - s.ta)) * tile;
 }
 
+// The factor that turns O, which is relative to its running maximum W and scaled by 2^shift, into the answer: 2^(W - Z - shift)
+// over the denominator L (relative to Z) with the sink's term.  A sink above Z becomes the reference, so that weights
+// far below its own keep their ratio to it.  0 for a row that saw nothing.
+__device__ __forceinline__ float answer_factor(float W, float Z, float L, const float* sinks, int head, float shift) {
+  if (Z == kNone && L == 0.f) return 0.f;
+  if (sinks) {
+    const float s = sinks[head] * kLog2e, ref = fmaxf(Z, fminf(s, -kNone));
+    L = L * exp2f(Z - ref) + exp2f(s - ref);
+    Z = ref;
+  }
+  return exp2f(W - Z - shift) / L;
+}
+
 // Floats of one partial record: O [rows][D], then mw, mz, l per row.
 __host__ __device__ constexpr size_t record_floats(int rows, int D) { return (size_t)rows * (D + 3); }
 
@@ -250,8 +263,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
       for (int q = 0; q < who.y - who.x; ++q) add(rest + ((size_t)q * 2 * cs.groups + g) * floats);
     }
     const int head = s.h * a.G + gr;
-    if (a.sinks) L += exp2f(a.sinks[head] * kLog2e - Z);
-    const float f = Z == kNone && !(L != L) ? 0.f : exp2f(W - Z - cs.shift) / L;
+    const float f = answer_factor(W, Z, L, a.sinks, head, cs.shift);
     const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
     const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
     store_act4(a.out + at * act_bytes(a.act_fmt), a.act_fmt, 0, out);

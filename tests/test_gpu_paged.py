@@ -299,6 +299,17 @@ def test_large_logits_on_pages_of_small_values(act, Tq, H, order, repeat):
     _close(*_attend(cache, table, [n - Tq], None, Tq, H, act, rng=rng, q=_along(rng, Tq, H, D)))
 
 
+@pytest.mark.parametrize("act,Tq,H", [("bf16", 1, 4), ("f32", 3, 4), ("bf16", 40, 8), ("bf16", 300, 1)])
+@pytest.mark.parametrize("pages", [8, 300])
+def test_sinks_far_above_logits_whose_values_are_large(act, Tq, H, pages):
+    """Weights of 2^-140 and less beside the sink's, on pages whose scale makes their sum an ordinary number."""
+    rng = np.random.default_rng(pages)
+    cache, table = _logit_pages(rng, 16, 64, [0, 16] * (pages // 2), [2.0 ** 100, 2.0 ** 90] * (pages // 2))
+    sinks = np.array([97.0, 104.0, 111.0, 132.0] * 2)[:H]
+    n = 16 * pages
+    _close(*_attend(cache, table, [n - Tq], None, Tq, H, act, sinks=sinks, rng=rng, q=_along(rng, Tq, H, 64)))
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("Tq,H", [(1, 4), (40, 8)])
 def test_key_scales_and_queries_far_from_one(act, Tq, H):
