@@ -597,8 +597,8 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
       }
       if (complete) {
         const int head = cw.s.h * a.G + gr;
-        const float f = answer_factor(W, Z, L, a.sinks, head, kShift);
-        const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+        const float2 f = answer_factors(W, Z, L, a.sinks, head, kShift);
+        const float out[4] = {v.x * f.x * f.y, v.y * f.x * f.y, v.z * f.x * f.y, v.w * f.x * f.y};
         const size_t at = (((size_t)cw.s.b * a.tok.Tq + j) * a.H + head) * D + c;
         store_act4(a.out + at * (F32 ? 4 : 2), F32 ? CSA_FMT_F32 : CSA_FMT_BF16, 0, out);
       } else {

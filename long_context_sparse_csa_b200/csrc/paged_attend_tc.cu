@@ -608,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       // the record of the last shared segment has been read
       if (!kPair && g == 1 && !warp_wait(&bars->recfree, (shared & 1u) ^ 1u)) return false;
       if (both && g == 0 && !warp_wait(&bars->recfull, shared & 1u)) return false;
-      float f = 1.f, f1 = 0.f;
+      float f = 1.f, f1 = 0.f, last = 1.f;
       if (direct && live) {                              // O relative to mw (and 2^kShift), the denominator to mz
         float W = mw, Z = mz, den = l;
         if (both) {
@@ -618,9 +618,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           den = l * exp2f(mz - Z) + other[(size_t)kRowTile * (D + 2) + rr] * exp2f(z1 - Z);
           f1 = exp2f(w1 - W);
         }
-        const float top = answer_factor(W, Z, den, a.sinks, head, kShift);
-        f = exp2f(mw - W) * top;
-        f1 *= top;
+        const float2 top = answer_factors(W, Z, den, a.sinks, head, kShift);
+        f = exp2f(mw - W) * top.x;
+        f1 *= top.x;
+        last = top.y;
       }
       uint8_t* out = a.out + 2 * ((((size_t)cur.s.b * a.tok.Tq + j) * a.H + head) * D);
 #pragma unroll 1
@@ -646,6 +647,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
               v[0] = fmaf(x0.x, f1, v[0]); v[1] = fmaf(x0.y, f1, v[1]); v[2] = fmaf(x0.z, f1, v[2]); v[3] = fmaf(x0.w, f1, v[3]);
               v[4] = fmaf(x1.x, f1, v[4]); v[5] = fmaf(x1.y, f1, v[5]); v[6] = fmaf(x1.z, f1, v[6]); v[7] = fmaf(x1.w, f1, v[7]);
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] *= last;
             uint4 y;
             y.x = (uint32_t)f_to_bf16_bits(v[0]) | ((uint32_t)f_to_bf16_bits(v[1]) << 16);
             y.y = (uint32_t)f_to_bf16_bits(v[2]) | ((uint32_t)f_to_bf16_bits(v[3]) << 16);

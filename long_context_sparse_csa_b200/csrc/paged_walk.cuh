@@ -201,17 +201,19 @@ __device__ __forceinline__ int tile_pos(const Seg& s, int i, int tile) {
   return (i < s.ta ? i : s.tb + (i - s.ta)) * tile;
 }
 
-// The factor that turns O, which is relative to its running maximum W and scaled by 2^shift, into the answer: 2^(W - Z - shift)
-// over the denominator L (relative to Z) with the sink's term.  A sink above Z becomes the reference, so that weights
-// far below its own keep their ratio to it.  0 for a row that saw nothing.
-__device__ __forceinline__ float answer_factor(float W, float Z, float L, const float* sinks, int head, float shift) {
-  if (Z == kNone && L == 0.f) return 0.f;
+// The factors that turn O, which is relative to its running maximum W and scaled by 2^shift, into the answer O * x * y:
+// 2^(W - Z - shift) over the denominator L (relative to Z) with the sink's term.  A sink above Z becomes the reference, so
+// that weights far below its own keep their ratio to it.  y is about the root of 2^(W - Z), a power of two: one factor
+// would lose its digits below 2^-126 where all values' scales are near 2^-126.  0 for a row that saw nothing.
+__device__ __forceinline__ float2 answer_factors(float W, float Z, float L, const float* sinks, int head, float shift) {
+  if (Z == kNone && L == 0.f) return make_float2(0.f, 0.f);
   if (sinks) {
     const float s = sinks[head] * kLog2e, ref = fmaxf(Z, fminf(s, -kNone));
     L = L * exp2f(Z - ref) + exp2f(s - ref);
     Z = ref;
   }
-  return exp2f(W - Z - shift) / L;
+  const float e = rintf(fminf(fmaxf(0.5f * (W - Z), -126.f), 126.f));
+  return make_float2(exp2f(W - Z - e - shift) / L, __uint_as_float((uint32_t)((int)e + 127) << 23));
 }
 
 // Floats of one partial record: O [rows][D], then mw, mz, l per row.
@@ -263,8 +265,8 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
       for (int q = 0; q < who.y - who.x; ++q) add(rest + ((size_t)q * 2 * cs.groups + g) * floats);
     }
     const int head = s.h * a.G + gr;
-    const float f = answer_factor(W, Z, L, a.sinks, head, cs.shift);
-    const float out[4] = {v.x * f, v.y * f, v.z * f, v.w * f};
+    const float2 f = answer_factors(W, Z, L, a.sinks, head, cs.shift);
+    const float out[4] = {v.x * f.x * f.y, v.y * f.x * f.y, v.z * f.x * f.y, v.w * f.x * f.y};
     const size_t at = (((size_t)s.b * a.tok.Tq + j) * a.H + head) * D + c;
     store_act4(a.out + at * act_bytes(a.act_fmt), a.act_fmt, 0, out);
   }

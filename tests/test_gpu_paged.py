@@ -310,6 +310,20 @@ def test_sinks_far_above_logits_whose_values_are_large(act, Tq, H, pages):
     _close(*_attend(cache, table, [n - Tq], None, Tq, H, act, sinks=sinks, rng=rng, q=_along(rng, Tq, H, 64)))
 
 
+@pytest.mark.parametrize("act,Tq,H", [("bf16", 1, 4), ("f32", 3, 4), ("bf16", 40, 8), ("bf16", 300, 1)])
+@pytest.mark.parametrize("n", [300, 6400])
+def test_value_scales_at_the_lower_end_keep_their_digits(act, Tq, H, n):
+    """Outputs near 2^-118 are ordinary numbers of their type: the bound is the usual one, without its constant but
+    for half of the type's smallest step (2^-134 for bf16, 2^-150 for float32) and one of float32."""
+    rng = np.random.default_rng(n)
+    N = -(-n // 16)
+    cache = Cache(rng, N, 1, 16, 64)
+    table, _ = _table(rng, 1, N, N, [N])
+    cache.vs[:] = 2.0 ** rng.integers(-126, -124, cache.vs.shape)
+    got, ref, tol = _attend(cache, table, [n - Tq], None, Tq, H, act, rng=rng)
+    _close(got, ref, tol - 1e-37 + 2.0 ** -149 + (2.0 ** -134 if act == "bf16" else 2.0 ** -150))
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("Tq,H", [(1, 4), (40, 8)])
 def test_key_scales_and_queries_far_from_one(act, Tq, H):
