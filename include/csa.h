@@ -569,6 +569,15 @@ CSA_API csa_status_t csa_paged_attend(const csa_gqa_t* L, const csa_page_pool_t*
                                       const int64_t* start, const int32_t* n_new, int32_t Tq, int64_t n_max,
                                       void* out, void* workspace, size_t ws_bytes, void* stream);
 
+/* Test aid: the second launch of csa_paged_attend alone, which joins the parts of the sequences that were cut, over what
+ * the workspace holds from an earlier call with the same arguments.  From byte 256 on the workspace has two int32 per
+ * (sequence, block of query rows, KV head), the first and the last CTA with a part (equal: nothing to join).  They are the
+ * first launch's; where one of its waits gave up (error bit 1) an entry may be an earlier call's bytes, and one that names
+ * no CTA is left out, its rows as they were. */
+CSA_API csa_status_t csa_debug_paged_join(const csa_gqa_t* L, const csa_page_table_t* T, const float* sinks,
+                                          const int64_t* start, const int32_t* n_new, int32_t Tq, int64_t n_max,
+                                          void* out, void* workspace, size_t ws_bytes, void* stream);
+
 /* Row dst[i] of the table becomes a copy of row src[i] (i < n; both int32 on the device), so that the
  * two share their pages; the pages row dst[i] held before are released.  Pairs are taken from the rows
  * as they were before the call.  A pair whose src or dst is out of range, whose dst is a src of the

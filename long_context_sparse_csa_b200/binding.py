@@ -116,6 +116,7 @@ _SIGS = {
     "csa_paged_append": (ctypes.c_int, [_GQA, _POOL, _TABLE, _P, _P, _I64, _P, _P, _I32, _P]),
     "csa_paged_workspace_size": (_SZ, [_GQA, _TABLE, _I32, _I64]),
     "csa_paged_attend": (ctypes.c_int, [_GQA, _POOL, _TABLE, _P, _I64, _P, _P, _P, _I32, _I64, _P, _P, _SZ, _P]),
+    "csa_debug_paged_join": (ctypes.c_int, [_GQA, _TABLE, _P, _P, _P, _I32, _I64, _P, _P, _SZ, _P]),
     "csa_pages_fork": (ctypes.c_int, [_TABLE, _P, _P, _I32, _P]),
     "csa_pages_reserve": (ctypes.c_int, [_TABLE, _P, _P, _I32, _P, _P, _P, _P]),
     "csa_pages_free": (ctypes.c_int, [_TABLE, _P, _P, _I64, _P]),
@@ -507,6 +508,19 @@ def csa_paged_attend(G, pool, T, q, sinks, start, n_new, Tq, n_max, out, workspa
                                   _arg(start, "start", torch.int64, B, d), _arg(n_new, "n_new", torch.int32, B, d), Tq,
                                   n_max, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
                                   _raw_stream(stream, d)))
+
+
+def csa_debug_paged_join(G, T, sinks, start, n_new, Tq, n_max, out, workspace, stream=None):
+    """The join of cut sequences alone, over what an earlier csa_paged_attend left in the workspace (test aid)."""
+    d, B = _here(T), T.B
+    if _token_stride(out, "out", G, B, Tq, G.H, d) != G.H * G.D:
+        raise CsaError(1, "out must be contiguous")
+    if workspace.get_device() != d:
+        raise CsaError(1, f"the workspace is on {workspace.device}, not on device {d}")
+    _check(lib().csa_debug_paged_join(G, T, _arg(sinks, "sinks", torch.float32, G.H, d),
+                                      _arg(start, "start", torch.int64, B, d), _arg(n_new, "n_new", torch.int32, B, d),
+                                      Tq, n_max, out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                      _raw_stream(stream, d)))
 
 
 def csa_pages_fork(T, src, dst, n, stream=None):

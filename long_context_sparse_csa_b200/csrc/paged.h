@@ -97,7 +97,7 @@ struct PagedAttendArgs {
   // split work (see paged_attend.cu)
   int rb_max;               // row blocks per (sequence, KV head) at most
   int ctas;
-  int2* info;               // [B * rb_max * Hkv] zero between calls
+  int2* info;               // [B * rb_max * Hkv] first and last CTA of a cut segment, written by every call
   float* part;              // [ctas][2] records
 };
 struct PagedPlan {
@@ -108,7 +108,8 @@ struct PagedPlan {
 };
 PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms);
 // row_tile: 8 or 16
-cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, cudaStream_t s);
-cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, cudaStream_t s);
+cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, bool join_only, cudaStream_t s);
+// join_only: only the kernel that joins cut segments, over what the workspace holds (test aid)
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, bool join_only, cudaStream_t s);
 
 }  // namespace csa

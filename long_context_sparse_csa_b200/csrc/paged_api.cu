@@ -152,6 +152,49 @@ csa_status_t make_plan(const csa_gqa_t* L, const csa_page_table_t* T, int32_t Tq
   return CSA_OK;
 }
 
+// csa_paged_attend, or (join_only: no pool and no queries) its second launch alone.
+csa_status_t attend(const csa_gqa_t* L, const csa_page_pool_t* pool, const csa_page_table_t* T, const void* q,
+                    int64_t q_stride, const float* sinks, const int64_t* start, const int32_t* n_new, int32_t Tq,
+                    int64_t n_max, void* out, void* workspace, size_t ws_bytes, bool join_only, void* stream) {
+  PagedPlan p;
+  CSA_TRY(make_plan(L, T, Tq, n_max, &p));
+  CSA_TRY(check_table(T, false));
+  if (!join_only) {
+    CSA_TRY(check_pool(pool));
+    CSA_TRY(need_ptr(q, "q"));
+    CSA_TRY(check_stride(L, &q_stride, (int64_t)L->H * L->D, "q_stride"));
+  }
+  if (sinks) CSA_TRY(need_ptr(sinks, "sinks", 4));
+  CSA_TRY(check_tokens(start, n_new, Tq));
+  CSA_TRY(need_ptr(out, "out"));
+  if (!workspace) return fail(CSA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", p.total);
+  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(CSA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < p.total) return fail(CSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, p.total);
+  if (n_max == 0) return CSA_OK;
+  PagedAttendArgs a;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.T = page_args(T);
+  a.P = join_only ? PoolArgs{} : pool_args(pool);
+  a.tok = token_args(start, n_new, Tq);
+  a.H = L->H; a.Hkv = L->Hkv; a.G = L->H / L->Hkv; a.D = L->D; a.act_fmt = L->act_format;
+  // no position is n_max or more: a longer window shows the same keys, and keeps the kernels' sums within int32
+  a.window = L->window < n_max ? L->window : (int)n_max;
+  a.first = L->first;
+  a.scale_log2 = (L->softmax_scale > 0 ? L->softmax_scale : 1.0f / sqrtf((float)L->D)) * kLog2e;
+  a.n_max = (int)n_max;
+  a.q = static_cast<const uint8_t*>(q);
+  a.q_stride = q_stride;
+  a.sinks = sinks;
+  a.out = static_cast<uint8_t*>(out);
+  a.err = reinterpret_cast<int*>(ws);
+  a.rb_max = p.rb_max;
+  a.ctas = p.ctas;
+  a.info = reinterpret_cast<int2*>(ws + p.info);
+  a.part = reinterpret_cast<float*>(ws + p.part);
+  const cudaError_t e = launch_paged_attend(a, p, join_only, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? CSA_OK : cuda_fail(e, "paged attention launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -191,41 +234,13 @@ csa_status_t csa_paged_attend(const csa_gqa_t* L, const csa_page_pool_t* pool, c
                               const void* q, int64_t q_stride, const float* sinks, const int64_t* start,
                               const int32_t* n_new, int32_t Tq, int64_t n_max, void* out, void* workspace,
                               size_t ws_bytes, void* stream) {
-  PagedPlan p;
-  CSA_TRY(make_plan(L, T, Tq, n_max, &p));
-  CSA_TRY(check_table(T, false));
-  CSA_TRY(check_pool(pool));
-  CSA_TRY(need_ptr(q, "q"));
-  CSA_TRY(check_stride(L, &q_stride, (int64_t)L->H * L->D, "q_stride"));
-  if (sinks) CSA_TRY(need_ptr(sinks, "sinks", 4));
-  CSA_TRY(check_tokens(start, n_new, Tq));
-  CSA_TRY(need_ptr(out, "out"));
-  if (!workspace) return fail(CSA_ERR_WORKSPACE, "workspace is NULL (%zu bytes needed)", p.total);
-  if (reinterpret_cast<uintptr_t>(workspace) % 256) return fail(CSA_ERR_WORKSPACE, "workspace must be 256-byte aligned");
-  if (ws_bytes < p.total) return fail(CSA_ERR_WORKSPACE, "workspace %zu bytes < %zu needed", ws_bytes, p.total);
-  if (n_max == 0) return CSA_OK;
-  PagedAttendArgs a;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
-  a.T = page_args(T);
-  a.P = pool_args(pool);
-  a.tok = token_args(start, n_new, Tq);
-  a.H = L->H; a.Hkv = L->Hkv; a.G = L->H / L->Hkv; a.D = L->D; a.act_fmt = L->act_format;
-  // no position is n_max or more: a longer window shows the same keys, and keeps the kernels' sums within int32
-  a.window = L->window < n_max ? L->window : (int)n_max;
-  a.first = L->first;
-  a.scale_log2 = (L->softmax_scale > 0 ? L->softmax_scale : 1.0f / sqrtf((float)L->D)) * kLog2e;
-  a.n_max = (int)n_max;
-  a.q = static_cast<const uint8_t*>(q);
-  a.q_stride = q_stride;
-  a.sinks = sinks;
-  a.out = static_cast<uint8_t*>(out);
-  a.err = reinterpret_cast<int*>(ws);
-  a.rb_max = p.rb_max;
-  a.ctas = p.ctas;
-  a.info = reinterpret_cast<int2*>(ws + p.info);
-  a.part = reinterpret_cast<float*>(ws + p.part);
-  const cudaError_t e = launch_paged_attend(a, p, static_cast<cudaStream_t>(stream));
-  return e == cudaSuccess ? CSA_OK : cuda_fail(e, "paged attention launch");
+  return attend(L, pool, T, q, q_stride, sinks, start, n_new, Tq, n_max, out, workspace, ws_bytes, false, stream);
+}
+
+csa_status_t csa_debug_paged_join(const csa_gqa_t* L, const csa_page_table_t* T, const float* sinks,
+                                  const int64_t* start, const int32_t* n_new, int32_t Tq, int64_t n_max, void* out,
+                                  void* workspace, size_t ws_bytes, void* stream) {
+  return attend(L, nullptr, T, nullptr, 0, sinks, start, n_new, Tq, n_max, out, workspace, ws_bytes, true, stream);
 }
 
 csa_status_t csa_pages_fork(const csa_page_table_t* T, const int32_t* src, const int32_t* dst, int32_t n,

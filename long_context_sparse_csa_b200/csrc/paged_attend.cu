@@ -661,27 +661,30 @@ bool make_pool_map(CUtensorMap* m, const void* base, const PagedAttendArgs& a, i
 }
 
 template <int D, int NT, bool F32>
-cudaError_t launch_warp_path(const PagedAttendArgs& a, cudaStream_t s) {
-  CUtensorMap km, vm;
-  if (!make_pool_map(&km, a.P.k, a, kSub) || !make_pool_map(&vm, a.P.v, a, kSub)) return cudaErrorInvalidValue;
-  auto kernel = paged_attend_kernel<D, NT, F32>;
-  cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Shape<D, NT, F32>::kBytes);
-  if (e == cudaSuccess)
-    e = launch_kernel(kernel, dim3(a.ctas), dim3(Shape<D, NT, F32>::kThreads), Shape<D, NT, F32>::kBytes, s, 0, a, km, vm);
+cudaError_t launch_warp_path(const PagedAttendArgs& a, bool join_only, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (!join_only) {
+    CUtensorMap km, vm;
+    if (!make_pool_map(&km, a.P.k, a, kSub) || !make_pool_map(&vm, a.P.v, a, kSub)) return cudaErrorInvalidValue;
+    auto kernel = paged_attend_kernel<D, NT, F32>;
+    e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), Shape<D, NT, F32>::kBytes);
+    if (e == cudaSuccess)
+      e = launch_kernel(kernel, dim3(a.ctas), dim3(Shape<D, NT, F32>::kThreads), Shape<D, NT, F32>::kBytes, s, 0, a, km, vm);
+  }
   if (e == cudaSuccess) e = launch_combine<D>(a, CombineShape{8 * NT, kTile, Shape<D, NT, F32>::kWarps, 1, F32 ? 15.f : 7.f}, s);
   return e;
 }
 
 }  // namespace
 
-cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, cudaStream_t s) {
+cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, bool join_only, cudaStream_t s) {
   const bool f32 = a.act_fmt == CSA_FMT_F32;
   if (a.D == 128) {
-    if (f32) return row_tile == 8 ? launch_warp_path<128, 1, true>(a, s) : launch_warp_path<128, 2, true>(a, s);
-    return row_tile == 8 ? launch_warp_path<128, 1, false>(a, s) : launch_warp_path<128, 2, false>(a, s);
+    if (f32) return row_tile == 8 ? launch_warp_path<128, 1, true>(a, join_only, s) : launch_warp_path<128, 2, true>(a, join_only, s);
+    return row_tile == 8 ? launch_warp_path<128, 1, false>(a, join_only, s) : launch_warp_path<128, 2, false>(a, join_only, s);
   }
-  if (f32) return row_tile == 8 ? launch_warp_path<64, 1, true>(a, s) : launch_warp_path<64, 2, true>(a, s);
-  return row_tile == 8 ? launch_warp_path<64, 1, false>(a, s) : launch_warp_path<64, 2, false>(a, s);
+  if (f32) return row_tile == 8 ? launch_warp_path<64, 1, true>(a, join_only, s) : launch_warp_path<64, 2, true>(a, join_only, s);
+  return row_tile == 8 ? launch_warp_path<64, 1, false>(a, join_only, s) : launch_warp_path<64, 2, false>(a, join_only, s);
 }
 
 }  // namespace csa

@@ -995,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
 }
 
 template <int D, bool kPair, int kW>
-cudaError_t launch_tc_as(const PagedAttendArgs& a, cudaStream_t s) {
+cudaError_t launch_tc_as(const PagedAttendArgs& a, bool join_only, cudaStream_t s) {
   auto kernel = paged_attend_tc_kernel<D, kPair, kW>;
   // the warps' register split draws on what the block was launched with: looked at once
   static const int regs = [&] {
@@ -1004,15 +1004,15 @@ cudaError_t launch_tc_as(const PagedAttendArgs& a, cudaStream_t s) {
   }();
   if (regs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
   cudaError_t e = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), TcShape<D>::kBytes);
-  if (e == cudaSuccess) e = launch_kernel(kernel, dim3(a.ctas), dim3(kThreads), TcShape<D>::kBytes, s, 0, a);
+  if (e == cudaSuccess && !join_only) e = launch_kernel(kernel, dim3(a.ctas), dim3(kThreads), TcShape<D>::kBytes, s, 0, a);
   if (e == cudaSuccess)
     e = launch_combine<D>(a, CombineShape{kPair ? 256 : 128, kKeys, 1, kPair ? 1 : 2, kShift}, s);
   return e;
 }
 
 template <int D, bool kPair>
-cudaError_t launch_tc(const PagedAttendArgs& a, cudaStream_t s) {
-  return a.T.page == 16 ? launch_tc_as<D, kPair, 16>(a, s) : launch_tc_as<D, kPair, 32>(a, s);
+cudaError_t launch_tc(const PagedAttendArgs& a, bool join_only, cudaStream_t s) {
+  return a.T.page == 16 ? launch_tc_as<D, kPair, 16>(a, join_only, s) : launch_tc_as<D, kPair, 32>(a, join_only, s);
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
@@ -1038,10 +1038,10 @@ PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_ma
   return p;
 }
 
-cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, cudaStream_t s) {
-  if (p.path == 1) return launch_paged_attend_warp(a, p.row_tile, s);
-  if (a.D == 128) return p.row_tile == 256 ? launch_tc<128, true>(a, s) : launch_tc<128, false>(a, s);
-  return p.row_tile == 256 ? launch_tc<64, true>(a, s) : launch_tc<64, false>(a, s);
+cudaError_t launch_paged_attend(const PagedAttendArgs& a, const PagedPlan& p, bool join_only, cudaStream_t s) {
+  if (p.path == 1) return launch_paged_attend_warp(a, p.row_tile, join_only, s);
+  if (a.D == 128) return p.row_tile == 256 ? launch_tc<128, true>(a, join_only, s) : launch_tc<128, false>(a, join_only, s);
+  return p.row_tile == 256 ? launch_tc<64, true>(a, join_only, s) : launch_tc<64, false>(a, join_only, s);
 }
 
 }  // namespace csa

@@ -236,6 +236,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const __grid_constan
   const int seg = blockIdx.x, rows = cs.rows;
   const int2 who = a.info[seg];
   if (who.x >= who.y) return;                                 // one CTA had all of it, or there was nothing
+  if (who.x < 0 || who.y >= a.ctas) return;                   // never written: a wait gave up, and was reported
   Seg s;
   seg_load(a, s, seg / a.Hkv, rows, cs.tile, cs.per);
   s.h = seg % a.Hkv;

@@ -417,6 +417,34 @@ def test_ctas_with_several_short_segments(Tq, H, Hkv, D):
     _close(*_attend(cache, table, start, rng.integers(0, Tq + 1, B), Tq, H, rng=rng))
 
 
+@pytest.mark.parametrize("act,Tq,H", [("bf16", 1, 4), ("bf16", 4, 4), ("f32", 1, 4), ("bf16", 20, 4), ("bf16", 300, 1)])
+def test_the_join_leaves_out_entries_that_name_no_cta(act, Tq, H):
+    """A first launch whose wait gave up can leave an earlier call's bytes where the join looks for the first and last
+    CTA of a sequence.  What names CTAs is joined; what does not is left alone, nothing is read out of range."""
+    rng = np.random.default_rng(18)
+    page, D, n = 128, 64, 60000
+    N = -(-n // page)
+    cache = Cache(rng, N, 1, page, D)
+    pool, dt = cache.up(), torch.float32 if act == "f32" else torch.bfloat16
+    T, G = C.make_page_table(_dev(np.arange(N, dtype=np.int32)[None]), _ints(N, 0), page), C.make_gqa(H, 1, D, act_format=act)
+    q = torch.randn(1, Tq, H, D, device="cuda").to(dt)
+    ws = torch.zeros(C.csa_paged_workspace_size(G, T, Tq, n), dtype=torch.uint8, device="cuda")
+    start, want = torch.tensor([n - Tq], device="cuda"), torch.full_like(q, 7.0)
+    C.csa_paged_attend(G, pool, T, q, None, start, None, Tq, n, want, ws)
+    blocks = -(-Tq * H // 256) if Tq * H > 128 else 1
+    entries = ws[256:256 + 8 * blocks].view(torch.int32).view(blocks, 2)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert (entries[:, 0] >= 0).all() and (entries[:, 1] > entries[:, 0]).all() and (entries[:, 1] < sms).all()
+    out = torch.full_like(q, 7.0)
+    C.csa_debug_paged_join(G, T, None, start, None, Tq, n, out, ws)
+    assert torch.equal(out, want)
+    out.fill_(7.0)
+    for bad in ((-1, 3), (-2 ** 31, 2 ** 31 - 1), (0, sms), (sms, sms + 1), (0x3F800000, 0x40000000), (5, 5), (9, 2)):
+        entries[:] = torch.tensor(bad, dtype=torch.int32, device="cuda")
+        C.csa_debug_paged_join(G, T, None, start, None, Tq, n, out, ws)
+        assert (out == 7.0).all(), bad
+
+
 def test_offsets_behind_2_31_bytes():
     """A pool of more than 2^32 bytes: the pages in use are its last."""
     Hkv, page, D, N = 8, 128, 128, 36000
