@@ -693,10 +693,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       if (!more) break;
       any = true;
       ++nparts;
-      // Eight softmax warps let go of every tile's entry, so that neither group falls a ring behind the other: both
-      // groups' where both work on it, else the group's own warps twice; of a part's only tile, again both groups'.
-      const uint32_t shares = kPair || cur.tiles == 1 ? 1u : 2u;
-      if (!kPair && g == 1 && cur.tiles == 1 && lane == 0) mbar_arrive(&bars->mfree[tile0 % kMeta]);
+      // Eight softmax warps let go of every tile's entry: both groups' of a tile that both work on and of a part's
+      // first tile, which both wait for; else the group's own warps twice.  So an entry that a group waits for is not
+      // published again before it has waited, and neither group falls a ring behind the other.
+      if (!kPair && g == 1 && lane == 0) mbar_arrive(&bars->mfree[tile0 % kMeta]);
       jobs = kPair ? cur.tiles : (cur.tiles - g + 1) / 2;
       mw = mz = kNone;
       l = 0.f;
@@ -784,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           if (!idle && ((c == 0 && !again) || step(std::false_type(), tile, sb, meta))) { why = kRange; break; }
           tc_fence_before();
           mbar_arrive(&bars->pfull[g][buf]);
-          if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
+          if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], kPair || tile == tile0 ? 1u : 2u);
           seen = again = false;
           ++job;
           ++c;
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
           if (c > 0 && !step(std::true_type(), tile, sb, meta)) {
             tc_fence_before();
             mbar_arrive(&bars->pfull[g][buf]);
-            if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], shares);
+            if ((c & 1) && lane == 0) mbar_arrive_n(&bars->mfree[tile % kMeta], kPair || tile == tile0 ? 1u : 2u);
             ++job;
             ++c;
             continue;

@@ -445,6 +445,27 @@ def test_the_join_leaves_out_entries_that_name_no_cta(act, Tq, H):
         assert (out == 7.0).all(), bad
 
 
+@pytest.mark.parametrize("Hkv,D,window", [(8, 64, 0), (6, 128, 300)])
+def test_parts_that_begin_at_every_place_of_the_ring(Hkv, D, window):
+    """Blocks of 128 rows, where two groups take the key tiles in turns: CTAs with many parts of one to nine tiles, so
+    that parts begin at every entry of the ring of looked-up tiles; called again and again, the results are the same."""
+    rng = np.random.default_rng(Hkv)
+    B, Tq, page = 42, 20, 32
+    start = rng.integers(0, 9 * 128 - Tq, B)
+    held = [-(-(s + Tq) // page) for s in start]
+    cache = Cache(rng, sum(held), Hkv, page, D)
+    table, _ = _table(rng, B, max(held), cache.N, held)
+    _close(*_attend(cache, table, start, None, Tq, Hkv, window=window, rng=rng))
+    T, G = C.make_page_table(_dev(table), _ints(cache.N, 0), page), C.make_gqa(Hkv, Hkv, D, window)
+    pool, q, n_max = cache.up(), torch.randn(B, Tq, Hkv, D, device="cuda").bfloat16(), table.shape[1] * page
+    ws = torch.zeros(C.csa_paged_workspace_size(G, T, Tq, n_max), dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(q) for _ in range(50)]
+    for out in outs:
+        C.csa_paged_attend(G, pool, T, q, None, _dev(start), None, Tq, n_max, out, ws)
+    assert C.csa_device_error(ws) == 0
+    assert all(torch.equal(out, outs[0]) for out in outs)
+
+
 def test_offsets_behind_2_31_bytes():
     """A pool of more than 2^32 bytes: the pages in use are its last."""
     Hkv, page, D, N = 8, 128, 128, 36000
