@@ -47,6 +47,10 @@ using namespace sm100;
 
 constexpr int kTile = 32;                     // keys per warp step
 constexpr int kSub = 16;                      // keys per TMA box: within one page
+// A warp's steps between two times that its sums go to the CTA's record: the tensor core cuts its sums off instead of
+// rounding them (one chain over 8,388,608 keys shared by 12 warps came out 6e-3 too small, more than bf16's half
+// step), the record is added up rounded.  Two products a step: 2e-4 at most.
+constexpr int kPieceSteps = 1024;
 
 struct Meta {                                 // one 16-key half of a ring stage
   float ks, vs;
@@ -225,14 +229,13 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
   float o[D / 16][NT][4];
   float mw[NT][2], mz[NT][2], l[NT][2];
   int tq[NT][2];                                              // positions of this lane's rows, -1: no such row
-  bool fresh = true;                                          // a segment begins
-  int seg_unit0 = 0;
+  bool fresh = true;                                          // a piece of a segment begins
+  int seg_unit0 = cw.unit;                                    // first unit of the segment's part
   int tmin = 0, tmax = 0;
   uint2 qr[S::kQRegs ? kWords : 1];
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
-      seg_unit0 = cw.unit;
       // the block's queries as f16 fragments: warp w takes rows w, w + 8, ...; a lane D / 32 dims
       __syncthreads();
       for (int r = warp; r < kRows; r += kWarps) {
@@ -525,9 +528,9 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
     __syncwarp();                                             // the stage has been read by every lane
     if (issued < steps && ok) issue();
 
-    // ---------------------------------------------------------------- the segment's end (for this CTA)
+    // ---------------------------------------------------------------- the segment's end (for this CTA), or a piece's
     const bool last_unit = cw.unit + 1 == cw.s.units;
-    if (!last_unit && step + 1 < steps) {
+    if (!last_unit && step + 1 < steps && (step + 1) % kPieceSteps != 0) {
       ++cw.unit;
       continue;
     }
@@ -576,41 +579,69 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
       __syncthreads();
     }
     const bool complete = seg_unit0 == 0 && last_unit;
+    const bool joined = step % kPieceSteps < cw.unit - seg_unit0;    // the record holds the part's earlier pieces
     const int seg = cw.sb * a.Hkv + cw.s.h;
     float* rec = a.part + ((size_t)blockIdx.x * 2 + (seg_unit0 == 0 ? 1 : 0)) * record_floats(kRows, D);
-    for (int i = tid; i < kRows * (D / 4); i += S::kThreads) {
-      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
-      const int R = cw.s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
-      if (j >= cw.s.n) continue;
-      float W = kNone, Z = kNone, L = 0.f;
+    // A row's maxima and denominator over the warps and, with earlier pieces, the record; factors of both O.
+    auto row_stats = [&](int r, float& W, float& Z, float& L, float& f, float& f0) {
+      W = Z = kNone;
+      L = f0 = 0.f;
+      f = 1.f;
       for (int w = 0; w < kWarps; ++w) {
         W = fmaxf(W, stat[(0 * kWarps + w) * kRows + r]);
         Z = fmaxf(Z, stat[(1 * kWarps + w) * kRows + r]);
       }
+      const float top = W;
+      float z0 = kNone;
+      if (joined) {
+        const float w0 = rec[(size_t)kRows * D + r];
+        z0 = rec[(size_t)kRows * (D + 1) + r];
+        W = fmaxf(W, w0);
+        Z = fmaxf(Z, z0);
+        f = exp2f(top - W);
+        f0 = exp2f(w0 - W);
+      }
       for (int w = 0; w < kWarps; ++w)
         L += stat[(2 * kWarps + w) * kRows + r] * exp2f(stat[(1 * kWarps + w) * kRows + r] - Z);
+      if (joined) L += rec[(size_t)kRows * (D + 2) + r] * exp2f(z0 - Z);
+    };
+    for (int i = tid; i < kRows * (D / 4); i += S::kThreads) {
+      const int r = i / (D / 4), c = (i - r * (D / 4)) * 4;
+      const int R = cw.s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;
+      if (j >= cw.s.n) continue;
+      float W, Z, L, f, f0;
+      row_stats(r, W, Z, L, f, f0);
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int q = 0; q < S::kBufs; ++q) {
         const float4 b = *reinterpret_cast<const float4*>(merge + ((size_t)q * kRows + r) * D + c);
         v.x += b.x; v.y += b.y; v.z += b.z; v.w += b.w;
       }
+      if (joined) {
+        const float4 b = *reinterpret_cast<const float4*>(rec + (size_t)r * D + c);
+        v.x = fmaf(b.x, f0, v.x * f); v.y = fmaf(b.y, f0, v.y * f); v.z = fmaf(b.z, f0, v.z * f); v.w = fmaf(b.w, f0, v.w * f);
+      }
       if (complete) {
         const int head = cw.s.h * a.G + gr;
-        const float2 f = answer_factors(W, Z, L, a.sinks, head, kShift);
-        const float out[4] = {v.x * f.x * f.y, v.y * f.x * f.y, v.z * f.x * f.y, v.w * f.x * f.y};
+        const float2 x = answer_factors(W, Z, L, a.sinks, head, kShift);
+        const float out[4] = {v.x * x.x * x.y, v.y * x.x * x.y, v.z * x.x * x.y, v.w * x.x * x.y};
         const size_t at = (((size_t)cw.s.b * a.tok.Tq + j) * a.H + head) * D + c;
         store_act4(a.out + at * (F32 ? 4 : 2), F32 ? CSA_FMT_F32 : CSA_FMT_BF16, 0, out);
       } else {
         *reinterpret_cast<float4*>(rec + (size_t)r * D + c) = v;
-        if (c == 0) {
-          rec[(size_t)kRows * D + r] = W;
-          rec[(size_t)kRows * (D + 1) + r] = Z;
-          rec[(size_t)kRows * (D + 2) + r] = L;
-        }
       }
     }
-    if (seg_unit0 == 0 && tid == 0) {
+    if (!complete) {
+      float W, Z, L, f, f0;
+      if (tid < kRows) row_stats(tid, W, Z, L, f, f0);
+      if (joined) __syncthreads();                            // every thread has read the record's statistics
+      if (tid < kRows) {
+        rec[(size_t)kRows * D + tid] = W;
+        rec[(size_t)kRows * (D + 1) + tid] = Z;
+        rec[(size_t)kRows * (D + 2) + tid] = L;
+      }
+    }
+    if (seg_unit0 == 0 && tid == 0 && (last_unit || step + 1 == steps)) {
       // the CTA with the segment's first unit names the CTAs that share it: this one to the one that
       // has the segment's last unit
       int2 who = make_int2(0, 0);
@@ -624,6 +655,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
     if (step + 1 < steps) {
       walk_next(a, cw, kRows, kTile, kWarps);
       fresh = true;
+      if (last_unit) seg_unit0 = 0;
     }
   }
   if (!ok) {

@@ -68,17 +68,23 @@ struct __align__(16) TileMeta {
   uint32_t have;                              // bits: the 16 keys have a page
 };
 
-// A CTA's part of a segment.
+// The tensor core cuts its sums off instead of rounding them: one chain of products over 1,048,576 keys came out
+// 6.4e-3 too small, more than bf16's half step.  So a part of more tiles than this is worked through in pieces, whose
+// sums are added up rounded in the CTA's record (2,048 products: 2e-4 at most; 256 tiles take 0.7 ms, a piece's end 5 us).
+constexpr int kPieceTiles = 256;
+
+// A piece of a CTA's part of a segment.
 struct Part {
   Seg s;
-  int sb, unit0, tiles;                       // first tile, number of tiles
-  uint32_t tile0;                             // tiles of the CTA's run before it
-  bool complete;
+  int sb, part0, unit0, tiles;                // first tile of the part, of the piece; tiles of the piece
+  bool last;                                  // of the part's pieces
+  bool complete;                              // the last, of a part that is the whole segment
 };
 
 // Walks the parts of a CTA's run.  (units are single tiles here)
 struct Parts {
   Walk w;
+  int part0;
   int64_t left;
 };
 
@@ -220,6 +226,7 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 
 __device__ __forceinline__ void parts_start(const PagedAttendArgs& a, Parts& p, const Run& run, int row_tile) {
   walk_start(a, p.w, run, row_tile, kKeys, 1);
+  p.part0 = p.w.unit;
   p.left = run.u1 - run.u0;
 }
 
@@ -227,14 +234,18 @@ __device__ __forceinline__ bool parts_next(const PagedAttendArgs& a, Parts& p, P
   if (p.left <= 0) return false;
   out.s = p.w.s;
   out.sb = p.w.sb;
+  out.part0 = p.part0;
   out.unit0 = p.w.unit;
   const int rest = p.w.s.units - p.w.unit;
-  out.tiles = p.left < rest ? (int)p.left : rest;
-  out.complete = p.w.unit == 0 && out.tiles == rest;
+  const int mine = p.left < rest ? (int)p.left : rest;
+  out.tiles = mine < kPieceTiles ? mine : kPieceTiles;
+  out.last = out.tiles == mine;
+  out.complete = p.part0 == 0 && out.tiles == rest;
   p.left -= out.tiles;
   if (p.left > 0) {
     p.w.unit += out.tiles - 1;
     walk_next(a, p.w, row_tile, kKeys, 1);
+    if (out.last) p.part0 = p.w.unit;
   }
   return true;
 }
@@ -424,7 +435,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
             i = 0;
             parts_next(a, walk, pt, kRowTile);
             row_span(a, pt.s, kRowTile, &tmin, &tmax);
-            pt.tile0 = (uint32_t)(n0 + k);
             if (lane == 0) {
               part_ring[parts_so_far % kParts] = pt;
               if (parts_so_far == 0) mbar_arrive(&bars->part0);
@@ -584,20 +594,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
     auto finish = [&](const Part& cur) {
       // ---------------------------------------------------------------- the part's end
       const int seg = cur.sb * a.Hkv + cur.s.h;
-      if (g == 0 && row == 0 && cur.unit0 == 0) {
+      if (g == 0 && row == 0 && cur.part0 == 0 && cur.last) {
         int2 who = make_int2(0, 0);
         if (!cur.complete) {
-          const int64_t end = run.u1 + (cur.s.units - cur.tiles);            // one behind the segment's last unit
+          const int64_t end = run.u1 + (cur.s.units - cur.unit0 - cur.tiles);  // one behind the segment's last unit
           who = make_int2((int)blockIdx.x, (int)((end * run.ctas - 1) / run.total));
         }
         a.info[seg] = who;
       }
       // A whole segment is answered here.  With the same rows in both groups, group 1 hands its share to
       // group 0 through the CTA's record.
-      const bool both = !kPair && cur.complete && cur.tiles > 1;
+      const bool joined = cur.unit0 > cur.part0;         // the record holds the part's earlier pieces
+      const bool both = !kPair && cur.complete && (cur.tiles > 1 || joined);
       const bool direct = cur.complete && (kPair || g == 0);
       if (!kPair && cur.complete && g == 1 && !both) return true;
-      float* rec = a.part + (((size_t)blockIdx.x * 2 + (cur.unit0 == 0 ? 1 : 0)) * (kPair ? 1 : 2) + (kPair ? 0 : g)) *
+      float* rec = a.part + (((size_t)blockIdx.x * 2 + (cur.part0 == 0 ? 1 : 0)) * (kPair ? 1 : 2) + (kPair ? 0 : g)) *
                                 record_floats(kRowTile, D);
       const int rr = (kPair ? g * 128 : 0) + row;
       const bool live = j < cur.s.n;
@@ -608,7 +619,38 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       // the record of the last shared segment has been read
       if (!kPair && g == 1 && !warp_wait(&bars->recfree, (shared & 1u) ^ 1u)) return false;
       if (both && g == 0 && !warp_wait(&bars->recfull, shared & 1u)) return false;
-      float f = 1.f, f1 = 0.f, last = 1.f;
+      float f = 1.f, f0 = 0.f;
+      if (joined && live) {                              // rare: the earlier pieces join O, its maxima and denominator
+        const float w0 = rec[(size_t)kRowTile * D + rr], z0 = rec[(size_t)kRowTile * (D + 1) + rr];
+        const float W = fmaxf(mw, w0), Z = fmaxf(mz, z0);
+        l = l * exp2f(mz - Z) + rec[(size_t)kRowTile * (D + 2) + rr] * exp2f(z0 - Z);
+        f = exp2f(mw - W);
+        f0 = exp2f(w0 - W);
+        mw = W;
+        mz = Z;
+      }
+      if (joined) {
+#pragma unroll 1
+        for (int c = 0; c < D; c += 16) {
+          float o[16];
+          __syncwarp();
+          tmem_ld_32x32b_x16(o_addr + (uint32_t)c, o);
+          tmem_wait_ld();
+          uint32_t ow[16];
+#pragma unroll
+          for (int q = 0; q < 16; q += 4) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (live) x = *reinterpret_cast<const float4*>(rec + (size_t)rr * D + c + q);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ow[q + e] = __float_as_uint(fmaf(xs[e], f0, jobs > 0 ? o[q + e] * f : 0.f));
+          }
+          tmem_st_32x32b_x16(o_addr + (uint32_t)c, ow);
+        }
+        tmem_wait_st();
+      }
+      float f1 = 0.f, last = 1.f;
+      f = 1.f;
       if (direct && live) {                              // O relative to mw (and 2^kShift), the denominator to mz
         float W = mw, Z = mz, den = l;
         if (both) {
@@ -628,7 +670,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attend_tc_kernel(const __gr
       for (int c = 0; c < D; c += 32) {
         float o[32];
         __syncwarp();
-        if (jobs > 0) {
+        if (jobs > 0 || joined) {
           tmem_ld_32x32b_x32(o_addr + (uint32_t)c, o);
           tmem_wait_ld();
         } else {

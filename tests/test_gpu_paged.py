@@ -466,6 +466,41 @@ def test_parts_that_begin_at_every_place_of_the_ring(Hkv, D, window):
     assert all(torch.equal(out, outs[0]) for out in outs)
 
 
+@pytest.mark.parametrize("act,Tq,G,n", [("bf16", 1, 8, 1 << 23), ("bf16", 17, 1, 1 << 21), ("bf16", 200, 1, 1 << 20),
+                                        ("f32", 1, 3, 1 << 20)])
+def test_long_sums_are_not_cut_off(act, Tq, G, n):
+    """One sequence's keys under as many table rows as there are SMs, so that a CTA has all of them: chains of sums as
+    long as they get.  Values of one sign make a cut-off sum visible.  The bound is the usual one, and 2^-11 of the sum
+    for bf16's chains of at most 2,048 products, each of which may cut off 2^-22.  The first and last rows are checked
+    in float64."""
+    page, D = 128, 64
+    N, B = n // page, torch.cuda.get_device_properties(0).multi_processor_count
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(n + Tq)
+    f8 = torch.float8_e4m3fn
+    k = (torch.randn(N, 1, page, D, generator=gen, device="cuda") * 60).clamp_(-448, 448).to(f8)
+    v = (torch.rand(N, 1, page, D, generator=gen, device="cuda") * 300 + 100).to(f8)
+    ks, vs = (torch.full((N, 1), 2.0 ** e, device="cuda") for e in (-9, -8))
+    table = torch.arange(N, dtype=torch.int32, device="cuda").expand(B, N).contiguous()
+    T, L = C.make_page_table(table, _ints(N, 0), page), C.make_gqa(G, 1, D, act_format=act)
+    q = torch.randn(B, Tq, G, D, generator=gen, device="cuda").to(torch.float32 if act == "f32" else torch.bfloat16)
+    start = torch.full((B,), n - Tq, device="cuda")
+    ws = torch.zeros(C.csa_paged_workspace_size(L, T, Tq, n), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(q)
+    C.csa_paged_attend(L, C.make_page_pool(k, v, ks, vs), T, q, None, start, None, Tq, n, out, ws)
+    assert C.csa_device_error(ws) == 0
+    K, V = k.view(n, D), v.view(n, D)
+    step = 1 << 18
+    for b, j in ((0, 0), (B - 1, Tq - 1)):
+        Q, seen = q[b, j].double(), n - Tq + j + 1
+        z = torch.cat([Q @ (K[i:i + step].double() * 2.0 ** -9).T for i in range(0, n, step)], 1)[:, :seen] / D ** 0.5
+        logit = max(float((Q.abs() @ (K[i:i + step].double().abs() * 2.0 ** -9).T).max()) for i in range(0, n, step)) / D ** 0.5
+        p = torch.softmax(z, 1)
+        ref = sum(p[:, i:i + step] @ (V[i:min(i + step, seen)].double() * 2.0 ** -8) for i in range(0, seen, step)).cpu().numpy()
+        tol = _tolerance(act, ref, ref, logit) + (2.0 ** -11 * ref if act == "bf16" else 0)
+        _close(out[b, j].double().cpu().numpy(), ref, tol)
+
+
 def test_offsets_behind_2_31_bytes():
     """A pool of more than 2^32 bytes: the pages in use are its last."""
     Hkv, page, D, N = 8, 128, 128, 36000
