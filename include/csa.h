@@ -93,7 +93,8 @@ typedef enum csa_status {
   CSA_ERR_UNSUPPORTED = 2,     /* valid, but no kernel for this shape / format */
   CSA_ERR_WORKSPACE = 3,       /* workspace missing or smaller than csa_workspace_size() */
   CSA_ERR_CUDA = 4,            /* a CUDA runtime call failed (message in csa_last_error) */
-  CSA_ERR_DEVICE_TIMEOUT = 5   /* a kernel set a bit of the device error word (csa_device_error) */
+  CSA_ERR_DEVICE_TIMEOUT = 5,  /* a kernel set bit 1 or 2 of a device error word (csa_device_error) */
+  CSA_ERR_DEVICE_PAGE = 6      /* bit 4 alone was set: a paged-cache call left something out */
 } csa_status_t;
 
 enum {
@@ -185,15 +186,18 @@ CSA_API const char* csa_version(void);
 /* Reads and clears the device error words (synchronises the stream): the
  * workspace's word (workspace may be NULL: then it is skipped) and the
  * library's own word on the current device, where the kernels of the calls
- * that take no workspace (csa_append, csa_compress) report.  *code gets the
- * OR of the bits kernels set (0 = none):
+ * that take no workspace (csa_append, csa_compress) report.  With workspace
+ * NULL also the device's word of the paged-cache calls that take none; a
+ * call with a workspace leaves that one to whoever made those calls.  *code
+ * gets the OR of the bits kernels set (0 = none):
  *   1  a bounded wait (mbarrier / tensor-memory pipeline / cluster
  *      reduction) gave up; the results of that launch are incomplete;
  *   2  the multi-CTA top-k found its score histogram inconsistent with the
  *      scores; that row's top-k output is incomplete (padded with -1);
  *   4  a paged-cache call met an index out of range or a token without a page
  *      of its own and left it out (see the paged cache below).
- * Returns CSA_ERR_DEVICE_TIMEOUT if any bit was set. */
+ * Returns CSA_ERR_DEVICE_TIMEOUT if bit 1 or 2 was set, CSA_ERR_DEVICE_PAGE
+ * if bit 4 was set alone. */
 CSA_API csa_status_t csa_device_error(void* workspace, size_t ws_bytes, void* stream, int32_t* code);
 
 /* Test and diagnostic aids (no counterpart on the pages). */
@@ -496,9 +500,9 @@ CSA_API csa_status_t csa_prefill(const csa_layer_t* L, const csa_cache_t* cache,
  *
  * Errors on the device.  A page-table entry or page index of n_pages or more, a row index outside [0, B), a position
  * behind the table, a token without a page of its own, or a reference count that would fall below
- * zero sets bit 4 of the device error word (the workspace's for csa_paged_attend, the library's own
- * word for the calls without a workspace, see csa_device_error); the page or token concerned is left
- * out, nothing is read or written out of range.
+ * zero sets bit 4 of a device error word: the workspace's for csa_paged_attend, for the calls without a
+ * workspace one word per device that csa_device_error reads when it gets no workspace; the page or token
+ * concerned is left out, nothing is read or written out of range.
  * ============================================================================================ */
 
 /* One grouped-query attention layer over the cache. */

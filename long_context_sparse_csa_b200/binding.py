@@ -21,7 +21,7 @@ SEGMENT = {"error_word": 0, "scores": 1, "topk_histogram": 2, "topk": 3, "partia
 KIND = {"csa": 0, "hca": 1}
 OP = {"index_topk": 0, "sparse_attend": 1, "hca_attend": 2, "decode_step": 3, "prefill": 4, "decode_step_indexed": 5}
 STATUS = {0: "CSA_OK", 1: "CSA_ERR_INVALID_ARG", 2: "CSA_ERR_UNSUPPORTED", 3: "CSA_ERR_WORKSPACE",
-          4: "CSA_ERR_CUDA", 5: "CSA_ERR_DEVICE_TIMEOUT"}
+          4: "CSA_ERR_CUDA", 5: "CSA_ERR_DEVICE_TIMEOUT", 6: "CSA_ERR_DEVICE_PAGE"}
 
 
 class CsaError(RuntimeError):
@@ -287,11 +287,12 @@ def csa_launch_count() -> int:
 
 
 def csa_device_error(workspace, stream=None) -> int:
-    """OR of the workspace's error word (None: skipped) and the library's own word; both cleared."""
+    """OR of the workspace's error word and the library's own word; without a workspace (None), of the library's and
+    the word of the paged-cache calls that take none.  The words read are cleared."""
     code = _I32(0)
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     st = lib().csa_device_error(ptr(workspace), nbytes, _stream(stream), ctypes.byref(code))
-    if st not in (0, 5):
+    if st not in (0, 5, 6):
         _check(st)
     return code.value
 

@@ -12,6 +12,7 @@
 
 #include "csa.h"
 #include "kernels.h"
+#include "paged.h"
 
 using namespace csa;
 
@@ -464,19 +465,23 @@ csa_status_t csa_device_error(void* workspace, size_t ws_bytes, void* stream, in
   if (code) *code = 0;
   if (workspace && ws_bytes < 4) return fail(CSA_ERR_WORKSPACE, "workspace smaller than its error word");
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int* lib_word = nullptr;
+  int *lib_word = nullptr, *page_word = nullptr;
   cudaError_t e = library_error_word(&lib_word);
-  int32_t v[2] = {0, 0};
+  if (e == cudaSuccess && !workspace) e = page_error_word(&page_word);
+  int32_t v[3] = {0, 0, 0};
   if (e == cudaSuccess && workspace) e = cudaMemcpyAsync(&v[0], workspace, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaMemcpyAsync(&v[1], lib_word, 4, cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess && page_word) e = cudaMemcpyAsync(&v[2], page_word, 4, cudaMemcpyDeviceToHost, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e == cudaSuccess && v[0]) e = cudaMemsetAsync(workspace, 0, 4, s);
   if (e == cudaSuccess && v[1]) e = cudaMemsetAsync(lib_word, 0, 4, s);
+  if (e == cudaSuccess && v[2]) e = cudaMemsetAsync(page_word, 0, 4, s);
   if (e == cudaSuccess) e = cudaStreamSynchronize(s);
   if (e != cudaSuccess) return cuda_fail(e, "csa_device_error");
-  const int32_t bits = v[0] | v[1];
+  const int32_t bits = v[0] | v[1] | v[2];
   if (code) *code = bits;
-  return bits ? fail(CSA_ERR_DEVICE_TIMEOUT, "device error word 0x%x", bits) : CSA_OK;
+  if (!bits) return CSA_OK;
+  return fail(bits == kErrPage ? CSA_ERR_DEVICE_PAGE : CSA_ERR_DEVICE_TIMEOUT, "device error word 0x%x", bits);
 }
 
 csa_status_t csa_debug_workspace_segment(const csa_layer_t* L, int32_t op, int32_t Tq, int64_t entry_cap,

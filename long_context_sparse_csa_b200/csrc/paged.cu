@@ -10,6 +10,7 @@
 // the append of 16,384 tokens of 8 heads of 128 dims 25-29 us (100 MB: 3.5-4 TB/s), of one token of 64
 // sequences 5.3; the copy of 900 pages of 128 KB 45 us (236 MB: 5.2 TB/s).
 #include <cooperative_groups.h>
+#include <mutex>
 
 #include "paged.h"
 
@@ -21,6 +22,8 @@ namespace cg = cooperative_groups;
 
 constexpr int kCluster = 8;
 constexpr int kThreads = 1024;
+
+__device__ int g_page_error;
 
 __device__ __forceinline__ int tokens_of(const TokenArgs& t, int b) {
   const int n = t.n_new ? t.n_new[b] : t.Tq;
@@ -644,6 +647,24 @@ __global__ void __launch_bounds__(kCopyThreads) pages_copy_kernel(const __grid_c
 }
 
 }  // namespace
+
+cudaError_t page_error_word(int** p) {
+  static std::mutex mu;
+  static int* addr[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  std::lock_guard<std::mutex> lock(mu);
+  if (!addr[dev]) {
+    void* q = nullptr;
+    e = cudaGetSymbolAddress(&q, g_page_error);
+    if (e != cudaSuccess) return e;
+    addr[dev] = static_cast<int*>(q);
+  }
+  *p = addr[dev];
+  return cudaSuccess;
+}
 
 cudaError_t launch_paged_append(const PagedAppendArgs& a, cudaStream_t s) {
   const int vec = a.T.page * a.D / 8;                    // 128 .. 2048 vectors of 8 values per (page, head)

@@ -5,6 +5,11 @@
 
 namespace csa {
 
+// Device address, on the current device, of the word where the paged calls without a workspace report (kErrPage).  Apart
+// from the library's other word, which every csa_device_error reads and clears: it would take these reports from whoever
+// made the call.
+cudaError_t page_error_word(int** p);
+
 struct PageArgs {
   int32_t* table;           // [B][cap]
   int32_t* refs;            // [n_pages]; null only where a call allows it

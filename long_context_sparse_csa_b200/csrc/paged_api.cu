@@ -219,8 +219,8 @@ csa_status_t csa_paged_append(const csa_gqa_t* L, const csa_page_pool_t* pool, c
   a.kv_stride = kv_stride;
   a.kmax = (int)pages_touched_max(Tq, T->page);
   if ((int64_t)T->B * a.kmax > INT_MAX / 2 / L->Hkv) return fail(CSA_ERR_UNSUPPORTED, "Tq=%d of %d sequences", Tq, T->B);
-  cudaError_t e = library_error_word(&a.err);
-  if (e != cudaSuccess) return cuda_fail(e, "library error word");
+  cudaError_t e = page_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "page error word");
   e = launch_paged_append(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA_OK : cuda_fail(e, "paged append launch");
 }
@@ -251,8 +251,8 @@ csa_status_t csa_pages_fork(const csa_page_table_t* T, const int32_t* src, const
   CSA_TRY(need_ptr(src, "src", 4));
   CSA_TRY(need_ptr(dst, "dst", 4));
   int* err = nullptr;
-  cudaError_t e = library_error_word(&err);
-  if (e != cudaSuccess) return cuda_fail(e, "library error word");
+  cudaError_t e = page_error_word(&err);
+  if (e != cudaSuccess) return cuda_fail(e, "page error word");
   e = launch_pages_fork(page_args(T), src, dst, n, err, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA_OK : cuda_fail(e, "page fork launch");
 }
@@ -272,8 +272,8 @@ csa_status_t csa_pages_reserve(const csa_page_table_t* T, const int64_t* start, 
   a.copy_src = copy_src;
   a.copy_dst = copy_dst;
   a.missing = missing;
-  cudaError_t e = library_error_word(&a.err);
-  if (e != cudaSuccess) return cuda_fail(e, "library error word");
+  cudaError_t e = page_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "page error word");
   e = launch_pages_reserve(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA_OK : cuda_fail(e, "page reserve launch");
 }
@@ -286,8 +286,8 @@ csa_status_t csa_pages_free(const csa_page_table_t* T, const int64_t* keep, cons
   if (begin) CSA_TRY(need_ptr(begin, "begin", 8));
   if (first < 0) return fail(CSA_ERR_INVALID_ARG, "first=%lld", (long long)first);
   int* err = nullptr;
-  cudaError_t e = library_error_word(&err);
-  if (e != cudaSuccess) return cuda_fail(e, "library error word");
+  cudaError_t e = page_error_word(&err);
+  if (e != cudaSuccess) return cuda_fail(e, "page error word");
   e = launch_pages_free(page_args(T), keep, begin, first, err, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA_OK : cuda_fail(e, "page free launch");
 }
@@ -308,8 +308,8 @@ csa_status_t csa_pages_compact(const csa_page_table_t* T, int32_t max_moves, int
   a.move_src = move_src;
   a.move_dst = move_dst;
   a.count = count;
-  cudaError_t e = library_error_word(&a.err);
-  if (e != cudaSuccess) return cuda_fail(e, "library error word");
+  cudaError_t e = page_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "page error word");
   e = launch_pages_compact(a, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA_OK : cuda_fail(e, "page compact launch");
 }
@@ -333,8 +333,8 @@ csa_status_t csa_pages_copy(const csa_gqa_t* L, const csa_page_pool_t* pool, con
   a.dst = dst;
   a.count = count;
   a.n = n;
-  cudaError_t e = library_error_word(&a.err);
-  if (e != cudaSuccess) return cuda_fail(e, "library error word");
+  cudaError_t e = page_error_word(&a.err);
+  if (e != cudaSuccess) return cuda_fail(e, "page error word");
   e = launch_pages_copy(a, num_sms(), static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? CSA_OK : cuda_fail(e, "page copy launch");
 }

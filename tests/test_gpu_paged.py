@@ -599,6 +599,33 @@ def test_append_leaves_out_tokens_without_a_page_of_their_own():
         assert np.array_equal(a, b)
 
 
+def test_errors_of_the_paged_calls_reach_nobody_else():
+    """A token without a page is reported where no workspace is asked about, and by its own status; the check of another
+    call's workspace, and the decode step that checks its own, neither report nor clear it."""
+    from csa_synth import decode_inputs, get_workload
+    from long_context_sparse_csa_b200.state import LayerState
+
+    td, rd, T = _book(np.full((1, 2), -1, np.int32), np.zeros(4, np.int32), 16)
+    cache = Cache(np.random.default_rng(0), 4, 1, 16, 64)
+    pool, x = cache.up(), torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    bad = lambda: C.csa_paged_append(C.make_gqa(1, 1, 64), pool, T, x, x, _dev(np.array([3])), None, 1)  # noqa: E731
+    bad()
+    ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+    assert C.csa_device_error(ws) == 0
+    wl = get_workload("csa_decode_tiny_2k")
+    d = decode_inputs(wl)
+    st, L = LayerState.from_arrays(wl.layers[0], wl.B, d), wl.layers[0]
+    args = [_dev(d[k]) for k in ("q", "idx_q", "idx_q_scale", "head_w", "x_new", "g_new", "t")]
+    out = torch.zeros((1, L.H, L.D), dtype=torch.float32, device="cuda")
+    topk = torch.zeros((1, L.top_k), dtype=torch.int32, device="cuda")
+    assert C.csa_decode_step_scratch(st.L, st.cache(), st.params(), *args, out, topk, read_device_error=True) == 0
+    assert C.csa_device_error(None) == BAD_PAGE and C.csa_device_error(None) == 0
+    bad()
+    assert C.lib().csa_device_error(None, 0, C._stream(), None) == 6
+    ws.view(torch.int32)[0] = BAD_PAGE | 1
+    assert C.lib().csa_device_error(C.ptr(ws), 256, C._stream(), None) == 5
+
+
 # ----------------------------------------------------------------------------- bookkeeping
 def _book(table, refs, page):
     td, rd = _dev(table), _dev(refs)
