@@ -564,10 +564,12 @@ CSA_API size_t csa_paged_workspace_size(const csa_gqa_t* L, const csa_page_table
  *   out:   [B][Tq][H][D] act_format; the rows of tokens j >= n_new[b] are left as they are
  * Slots that no query sees are not read as numbers: whatever bytes they hold, NaN codes among them,
  * change nothing.  A NaN among the keys or values that a query sees makes that query's output NaN, at
- * least in the channels concerned.  Products and sums are float32 or wider; probabilities are rounded to
- * 11 bits for the product with the values (22 bits when act_format is float32), those below 2^-18 of a
- * query's largest to 2^-29 of it (float32: below 2^-17, to 2^-40).  Results depend on the arguments and the
- * number of SMs alone. */
+ * least in the channels concerned.  Products and sums are float32 or wider (logits too: their magnitude has to
+ * stay below 2^23).  What is rounded is w_i = p_i * (value scale of key i's page), the factor of key i's codes:
+ * to 11 bits, where it is below 2^-18 of the query's largest w to 2^-29 of that largest (act_format float32: to
+ * 22 bits, below 2^-17 to 2^-40).  Beside a page of a large scale, keys on pages of a far smaller one therefore
+ * lose digits in every channel, also in channels where the large page's codes are 0.  Results depend on the
+ * arguments and the number of SMs alone. */
 CSA_API csa_status_t csa_paged_attend(const csa_gqa_t* L, const csa_page_pool_t* pool, const csa_page_table_t* T,
                                       const void* q, int64_t q_stride, const float* sinks,
                                       const int64_t* start, const int32_t* n_new, int32_t Tq, int64_t n_max,

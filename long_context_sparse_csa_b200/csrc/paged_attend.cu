@@ -28,7 +28,7 @@
 // the scale, O sums 2^(z + v - mw), mw the running maximum of z + v, and the denominator sums
 // 2^(z - mz) with its own running maximum mz; both exponentials are cheap here, and neither can lose
 // the other's range however much the pages' scales differ.
-// P is f16 (11 bits): scaled by 2^7, with maxima that move only when a tile exceeds them by more than
+// P, relative to the largest probability times value scale, is f16 (11 bits): scaled by 2^7, with maxima that move only when a tile exceeds them by more than
 // 8, or (float32) by 2^15 with exact maxima and a second f16 term.  Rounding P is unbiased and f16
 // keeps all 11 bits down to 2^-21 (2^-29) of the largest weight.
 #include <cudaTypedefs.h>

@@ -6,7 +6,7 @@ import torch
 
 from long_context_sparse_csa_b200 import binding as C
 from oracle import paged as O
-from oracle.formats import e4m3_encode
+from oracle.formats import e4m3_decode, e4m3_encode
 
 pytestmark = pytest.mark.gpu
 BAD_PAGE = 4
@@ -322,6 +322,36 @@ def test_value_scales_at_the_lower_end_keep_their_digits(act, Tq, H, n):
     cache.vs[:] = 2.0 ** rng.integers(-126, -124, cache.vs.shape)
     got, ref, tol = _attend(cache, table, [n - Tq], None, Tq, H, act, rng=rng)
     _close(got, ref, tol - 1e-37 + 2.0 ** -149 + (2.0 ** -134 if act == "bf16" else 2.0 ** -150))
+
+
+@pytest.mark.parametrize("act,Tq,H", [("bf16", 1, 4), ("bf16", 4, 4), ("f32", 3, 4), ("bf16", 40, 8), ("bf16", 300, 1)])
+@pytest.mark.parametrize("down", [4, 12, 20, 30, 45])
+def test_a_page_of_large_values_in_one_channel(act, Tq, H, down):
+    """What is rounded is probability times value scale (w), so that a page whose values are large in one channel takes
+    digits from the others' keys in all channels: 11 bits (22 for float32) down to 2^-18 (2^-17) of the largest w, half
+    of 2^-29 (2^-40) of the largest w below that."""
+    rng = np.random.default_rng(down)
+    page, D, N = 16, 64, 24
+    cache = Cache(rng, N, 1, page, D, spread=1)
+    cache.k[:] = e4m3_encode(rng.integers(-1, 2, cache.k.shape) * 1.0)
+    cache.vs[:] = 2.0 ** -down
+    cache.vs[1::7] = 1.0
+    cache.v[1::7, ..., 1:] = 0
+    table, n = np.arange(N, dtype=np.int32)[None], N * page
+    q = rng.standard_normal((1, Tq, H, D)) * 4
+    got, ref, tol = _attend(cache, table, [n - Tq], None, Tq, H, act, rng=rng, q=q)
+    top, low = cache.vs.max(), 2.0 ** -30 if act == "bf16" else 2.0 ** -41
+    Q = torch.from_numpy(q).to(torch.float32 if act == "f32" else torch.bfloat16).double().numpy()[0]
+    K = e4m3_decode(cache.k[:, 0]).reshape(n, D) * np.repeat(cache.ks[:, 0], page)[:, None].astype(np.float64)
+    codes = np.abs(e4m3_decode(cache.v[:, 0])).reshape(n, D)
+    for j in range(Tq):
+        seen = n - Tq + j + 1
+        z = Q[j] @ K[:seen].T / np.sqrt(D)
+        p = np.exp(z - z.max(1, keepdims=True))
+        w = p / p.sum(1, keepdims=True) * np.repeat(cache.vs[:, 0], page)[:seen]
+        assert (w.max(1) <= top).all()
+        tol[j] += low * w.max(1)[:, None] * codes[:seen].sum(0)
+    _close(got, ref, tol)
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
