@@ -40,8 +40,8 @@
  *     read back by csa_device_error().
  *   - Workspace: csa_workspace_size() bytes of device memory, zero-filled by
  *     the caller before its FIRST use (the library leaves its counters and
- *     histograms at zero after every call; zero it again after a device
- *     error).  Concurrent calls must not share a workspace.
+ *     histograms at zero after every call but the paged cache's, whose
+ *     workspace is its own; zero it again after a device error).  Concurrent calls must not share a workspace.
  *   - Positions: q_pos[b * Tq + j] (device int64) is the absolute position t
  *     of query token j of sequence b; raw row index r = t - pos0.
  *
@@ -548,7 +548,9 @@ CSA_API csa_status_t csa_paged_append(const csa_gqa_t* L, const csa_page_pool_t*
                                       const void* k_new, const void* v_new, int64_t kv_stride,
                                       const int64_t* start, const int32_t* n_new, int32_t Tq, void* stream);
 
-/* Workspace bytes of csa_paged_attend (host; 0 if an argument is invalid). */
+/* Workspace bytes of csa_paged_attend (host; 0 if an argument is invalid).  One workspace serves paged calls of all
+ * shapes that it is large enough for, one after the other.  It does not serve the other calls of the library: they need
+ * theirs at zero, and a paged call leaves its records in it (zero-fill it before such a use). */
 CSA_API size_t csa_paged_workspace_size(const csa_gqa_t* L, const csa_page_table_t* T, int32_t Tq, int64_t n_max);
 
 /* Attention over the cache.  The query at position t = start[b] + j sees key i of its sequence iff

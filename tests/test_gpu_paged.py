@@ -1000,6 +1000,35 @@ def test_one_workspace_for_calls_of_different_shapes():
     assert C.csa_device_error(shared) == 0
 
 
+def test_a_paged_workspace_that_is_zeroed_serves_the_other_calls():
+    """Both ways: the paged calls read nothing that others left but the error word, and after a zero-fill the others
+    find what they need."""
+    from csa_synth import decode_inputs, get_workload
+    from long_context_sparse_csa_b200.state import LayerState, to_device
+
+    wl = get_workload("csa_decode_128k", B=2, n=4 * 20000)
+    layer, d = wl.layers[0], decode_inputs(get_workload("csa_decode_128k", B=2, n=4 * 20000))
+    st = LayerState.from_arrays(layer, wl.B, d)
+    cap = d["entries"].shape[1]
+    rng = np.random.default_rng(19)
+    cache = Cache(rng, 90, 1, 16, 64)
+    table, _ = _table(rng, 1, 90, 90, [90])
+    pool, T, G = cache.up(), C.make_page_table(_dev(table), _ints(90, 0), 16), C.make_gqa(8, 1, 64)
+    q, start = torch.randn(1, 40, 8, 64, device="cuda").bfloat16(), torch.tensor([1400], device="cuda")
+    size = max(st.workspace("index_topk", 1, cap).numel(), C.csa_paged_workspace_size(G, T, 40, 1440))
+    args = [to_device(d[k]) for k in ("idx_q", "idx_q_scale", "head_w", "t")]
+    shared, want_o, want_k = torch.zeros(size, dtype=torch.uint8, device="cuda"), None, None
+    for _ in range(3):
+        topk = torch.zeros((2, layer.top_k), dtype=torch.int32, device="cuda")
+        C.csa_index_topk(st.L, st.cache(), *args, 1, cap, topk, None, shared)
+        out = torch.zeros_like(q)
+        C.csa_paged_attend(G, pool, T, q, None, start, None, 40, 1440, out, shared)
+        assert C.csa_device_error(shared) == 0
+        want_o, want_k = out if want_o is None else want_o, topk if want_k is None else want_k
+        assert torch.equal(out, want_o) and torch.equal(topk, want_k)
+        shared.zero_()
+
+
 def test_a_captured_chunk_follows_its_inputs():
     """Prompt chunks of a padded batch in a graph, replayed beside an eager call on another stream."""
     rng = np.random.default_rng(8)
