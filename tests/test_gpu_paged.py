@@ -559,6 +559,30 @@ def test_offsets_behind_2_31_bytes():
     _close(out.float().cpu().numpy(), ref, _tolerance("bf16", ref, w, z))
 
 
+@pytest.mark.parametrize("H,D", [(8, 128), (16, 64)])
+def test_offsets_behind_2_31_bytes_of_many_rows(H, D):
+    """The same for blocks of many query rows: 200 tokens written to and read from the last pages of such a pool."""
+    Hkv, page, Tq = 8, 128, 200
+    N, dev = 36000 * 128 // D, "cuda"
+    if torch.cuda.get_device_properties(0).total_memory < 20 << 30:
+        pytest.skip("needs 10 GB")
+    k = torch.zeros(N, Hkv, page, D, dtype=torch.uint8, device=dev)
+    v, sc = torch.zeros_like(k), torch.ones(N, Hkv, device=dev)
+    pool, start = C.make_page_pool(k, v, sc, sc.clone()), torch.tensor([0], device=dev)
+    table = torch.tensor([[N - 1, N - 3]], dtype=torch.int32, device=dev)
+    T, G = C.make_page_table(table, torch.zeros(N, dtype=torch.int32, device=dev), page), C.make_gqa(H, Hkv, D)
+    x, q = (torch.randn(1, Tq, h, D, device=dev).bfloat16() for h in (Hkv, H))
+    C.csa_paged_append(G, pool, T, x, x, start, None, Tq)
+    ws = torch.zeros(C.csa_paged_workspace_size(G, T, Tq, 256), dtype=torch.uint8, device=dev)
+    out = torch.zeros_like(q)
+    C.csa_paged_attend(G, pool, T, q, None, start, None, Tq, 256, out, ws)
+    assert C.csa_device_error(ws) == 0 and C.csa_device_error(None) == 0
+    at = [N - 1, N - 3]
+    ref, _, w, z = O.attend(k[at].cpu().numpy(), v[at].cpu().numpy(), *[p.cpu().numpy()[at] for p in pool.keep[2:]],
+                            np.array([[0, 1]]), page, q.float().cpu().numpy(), [0], None, 256)
+    _close(out.float().cpu().numpy(), ref, _tolerance("bf16", ref, w, z))
+
+
 # ----------------------------------------------------------------------------- append
 def _append(cache, table, refs, x, y, start, n_new, act):
     dt = torch.float32 if act == "f32" else torch.bfloat16
