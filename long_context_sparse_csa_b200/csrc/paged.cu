@@ -331,7 +331,7 @@ __device__ __forceinline__ ReserveEntry reserve_entry(const PagesReserveArgs& a,
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads, 1)
 pages_reserve_kernel(const __grid_constant__ PagesReserveArgs a) {
   __shared__ int scratch[32];
-  __shared__ int box[4][kCluster][2];
+  __shared__ int box[3][kCluster][2];
   __shared__ int32_t list[kListPer];
   cg::cluster_group cl = cg::this_cluster();
   const unsigned rank = cl.block_rank();

@@ -109,9 +109,9 @@ struct PagedPlan {
   int path;                 // 1: warp-level kernel, 2: tcgen05 kernel
   int row_tile;             // query rows (token, head of the group) per block
   int rb_max, ctas;
-  size_t info, info_bytes, part, part_bytes, total;
+  size_t info, part, total;
 };
-PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms);
+PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int num_sms);
 // row_tile: 8 or 16
 cudaError_t launch_paged_attend_warp(const PagedAttendArgs& a, int row_tile, bool join_only, cudaStream_t s);
 // join_only: only the kernel that joins cut segments, over what the workspace holds (test aid)

@@ -148,7 +148,7 @@ csa_status_t make_plan(const csa_gqa_t* L, const csa_page_table_t* T, int32_t Tq
   const int64_t rows = (int64_t)Tq * (L->H / L->Hkv);
   if (rows > INT_MAX || (rows / 8 + 1) * T->B * L->Hkv > INT_MAX)
     return fail(CSA_ERR_UNSUPPORTED, "%lld query rows per KV head of %d sequences", (long long)rows, T->B);
-  *p = paged_plan(L->act_format, T->B, L->H / L->Hkv, L->Hkv, L->D, Tq, (int)n_max, num_sms());
+  *p = paged_plan(L->act_format, T->B, L->H / L->Hkv, L->Hkv, L->D, Tq, num_sms());
   return CSA_OK;
 }
 

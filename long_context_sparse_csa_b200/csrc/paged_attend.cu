@@ -32,7 +32,6 @@
 // 8, or (float32) by 2^15 with exact maxima and a second f16 term.  Rounding P is unbiased and f16
 // keeps all 11 bits down to 2^-21 (2^-29) of the largest weight.
 #include <cudaTypedefs.h>
-#include <cuda_fp16.h>
 #include <limits.h>
 #include <mutex>
 
@@ -70,14 +69,6 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Four e4m3 codes as two pairs of f16 values, exactly; NaN codes become NaN.
-__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
 __device__ __forceinline__ void mma_f16(float c[4], const uint32_t a[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
@@ -89,11 +80,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
   return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
 }
 
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
@@ -109,9 +95,6 @@ __device__ __forceinline__ float exp2_of(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-
-// NaN codes of four e4m3 bytes as a mask of 0x80 bytes.
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 template <int D, int NT, bool F32>
 struct Shape {
@@ -236,7 +219,7 @@ paged_attend_kernel(const __grid_constant__ PagedAttendArgs a, const __grid_cons
   for (int step = 0; step < steps; ++step) {
     if (fresh) {
       fresh = false;
-      // the block's queries as f16 fragments: warp w takes rows w, w + 8, ...; a lane D / 32 dims
+      // the block's queries as f16 fragments: warp w takes rows w, w + kWarps, ...; a lane D / 32 dims
       __syncthreads();
       for (int r = warp; r < kRows; r += kWarps) {
         const int R = cw.s.rb * kRows + r, j = R / a.G, gr = R - j * a.G;

@@ -27,7 +27,6 @@
 // alternate tiles, joined at the end.  A group works through half tiles in two buffers of S: while it
 // weighs one, the other's scores are computed (one buffer of whole tiles: 1,460 us against 1,434).  P lies
 // over its S, so the next S there waits for the product that reads it.
-#include <cuda_fp16.h>
 #include <type_traits>
 
 #include "paged_walk.cuh"
@@ -108,20 +107,6 @@ struct TcShape {
 };
 
 __device__ __forceinline__ uint32_t sw128(int r, int j) { return (uint32_t)(r * 128 + ((j ^ (r & 7)) << 4)); }
-
-__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
-      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-}
-
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&h);
-}
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -1062,9 +1047,8 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 // Which kernel: the warp-level one for float32 activations and up to 16 query rows per KV head, tcgen05 above.
-PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_max, int num_sms) {
+PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int num_sms) {
   PagedPlan p;
-  (void)n_max;
   const int64_t rows = (int64_t)Tq * G;
   p.path = act_fmt == CSA_FMT_F32 || rows <= 16 ? 1 : 2;
   p.row_tile = p.path == 1 ? (rows <= 8 ? 8 : 16) : (rows <= 128 ? 128 : 256);
@@ -1072,11 +1056,9 @@ PagedPlan paged_plan(int act_fmt, int B, int G, int Hkv, int D, int Tq, int n_ma
   p.ctas = num_sms;
   size_t off = 256;                                           // the error word
   p.info = off;
-  p.info_bytes = (size_t)B * p.rb_max * Hkv * sizeof(int2);
-  off = up256(off + p.info_bytes);
+  off = up256(off + (size_t)B * p.rb_max * Hkv * sizeof(int2));
   p.part = off;
-  p.part_bytes = (size_t)p.ctas * 2 * record_floats(p.path == 1 ? p.row_tile : 256, D) * 4;
-  p.total = up256(off + p.part_bytes);
+  p.total = up256(off + (size_t)p.ctas * 2 * record_floats(p.path == 1 ? p.row_tile : 256, D) * 4);
   return p;
 }
 

@@ -8,6 +8,8 @@
 // lengths alone, so results do not change from run to run.
 #pragma once
 
+#include <cuda_fp16.h>
+
 #include "paged.h"
 
 namespace csa {
@@ -15,6 +17,22 @@ namespace csa {
 namespace {
 
 constexpr float kNone = -3.0e38f;             // a running maximum before any key: finite, below every logit
+
+// Four e4m3 codes as two pairs of f16 values, exactly; NaN codes become NaN.
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+// NaN codes of four e4m3 bytes as a mask of 0x80 bytes.
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&h);
+}
 
 // One segment's tiles: [0, ta) and [tb, te) in units of 32 positions.
 struct Seg {
