@@ -496,15 +496,17 @@ def test_parts_that_begin_at_every_place_of_the_ring(Hkv, D, window):
     assert all(torch.equal(out, outs[0]) for out in outs)
 
 
-@pytest.mark.parametrize("act,Tq,G,n", [("bf16", 1, 8, 1 << 23), ("bf16", 17, 1, 1 << 21), ("bf16", 200, 1, 1 << 20),
-                                        ("f32", 1, 3, 1 << 20)])
-def test_long_sums_are_not_cut_off(act, Tq, G, n):
-    """One sequence's keys under as many table rows as there are SMs, so that a CTA has all of them: chains of sums as
-    long as they get.  Values of one sign make a cut-off sum visible.  The bound is the usual one, and 2^-11 of the sum
+@pytest.mark.parametrize("act,Tq,G,n,B", [("bf16", 1, 8, 1 << 23, 0), ("bf16", 17, 1, 1 << 21, 0), ("bf16", 200, 1, 1 << 20, 0),
+                                          ("f32", 1, 3, 1 << 20, 0), ("bf16", 30, 3, 257 * 128, 0), ("bf16", 30, 3, 513 * 128, 0),
+                                          ("bf16", 200, 1, 257 * 128, 0), ("bf16", 20, 2, 22000 * 128, 3),
+                                          ("bf16", 300, 1, 11000 * 128, 3), ("bf16", 5, 2, 4800 * 128, 201), ("f32", 2, 2, 4800 * 128, 201)])
+def test_long_sums_are_not_cut_off(act, Tq, G, n, B):
+    """One sequence's keys under as many table rows as there are SMs (or B), so that a CTA has all of them: chains of sums
+    as long as they get; sums in several pieces, the last of one tile, and pieces of parts that begin or end elsewhere.  Values of one sign make a cut-off sum visible.  The bound is the usual one, and 2^-11 of the sum
     for bf16's chains of at most 2,048 products, each of which may cut off 2^-22.  The first and last rows are checked
     in float64."""
     page, D = 128, 64
-    N, B = n // page, torch.cuda.get_device_properties(0).multi_processor_count
+    N, B = n // page, B or torch.cuda.get_device_properties(0).multi_processor_count
     gen = torch.Generator(device="cuda")
     gen.manual_seed(n + Tq)
     f8 = torch.float8_e4m3fn
