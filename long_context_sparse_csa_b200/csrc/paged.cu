@@ -8,7 +8,8 @@
 // and whose shared memory holds the running counts, so that no scratch memory is needed.  Measured on
 // the device: fork 1.7-2.3 us, free 2, reserve 8-9 (512 rows, 50,000 pages), compact 7, all bound by latency;
 // the append of 16,384 tokens of 8 heads of 128 dims 25-29 us (100 MB: 3.5-4 TB/s), of one token of 64
-// sequences 5.3; the copy of 900 pages of 128 KB 45 us (236 MB: 5.2 TB/s).
+// sequences 5.3 (with its pages' bytes in memory 10 where no scale grows, 16 where 436 of 1,024 do: their earlier codes are
+// read and written in one more chain); the copy of 900 pages of 128 KB 45 us (236 MB: 5.2 TB/s).
 #include <cooperative_groups.h>
 #include <mutex>
 

@@ -4,8 +4,8 @@
 // What bounds it.  A decode step reads 2 D bytes per key and KV head and does 4 D G flops with them
 // (G query heads of the group): at G = 8 that is 16 flops a byte, so memory bounds it.  The design
 // keeps bytes in flight: 8 or 12 warps per SM, each with its own ring of 32-key tiles that TMA fills.
-// Measured, 64 heads on 8 KV heads of 128 dims: 1,048,576 keys in 361-379 us (5.7-5.9 TB/s, 0.86-0.91 of the
-// measured copy rate), 8 sequences of up to 131,072 in 268-276 us; about 640 instructions per tile and warp,
+// Measured, 64 heads on 8 KV heads of 128 dims: 1,048,576 keys in 337-368 us (5.8-6.4 TB/s, 0.89-0.97 of the
+// measured copy rate, from card to card), 8 sequences of up to 131,072 in 269-272 us; about 640 instructions per tile and warp,
 // half of them code conversions and byte permutes, leave little of the clock unused.
 //
 // Work.  A segment is one (sequence, block of query rows, KV head); a row is (token, head of the
