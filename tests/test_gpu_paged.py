@@ -222,6 +222,25 @@ def test_bytes_that_no_query_sees_change_nothing(act, Tq, H, window, first):
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("Tq,H", [(1, 4), (4, 4), (20, 4), (140, 2)])
+@pytest.mark.parametrize("scale", [np.nan, np.inf, 0.0, -1.0, 2.0 ** 120, 2.0 ** -126])
+def test_scales_that_no_query_sees_change_nothing(act, Tq, H, scale):
+    """Pages behind the window or behind the sequence that lie in tiles which are read."""
+    rng = np.random.default_rng(20)
+    page, D, total = 16, 64, 330 + Tq
+    held = -(-total // page) + 3
+    cache = Cache(rng, held, 1, page, D)
+    table, _ = _table(rng, 1, held, held, [held])
+    pos = np.arange(held) * page
+    hidden = ((pos + page - 1 <= 330 - 70) & (pos >= 5)) | (pos >= total)
+    g = table[0, hidden]
+    cache.ks[g], cache.vs[g], cache.k[g], cache.v[g] = scale, scale, 0x7F, 0x7F
+    got, ref, tol = _attend(cache, table, [330], None, Tq, H, act, 70, 5, rng=rng)
+    assert not np.isnan(ref).any()
+    _close(got, ref, tol)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("where", ["k", "v"])
 def test_a_nan_reaches_the_queries_that_see_it_and_no_other(act, where):
     rng = np.random.default_rng(10)
