@@ -5,7 +5,7 @@
 // tensor core, and beside it the exponentials (one per 4 D = 512 flops at D = 128: at 16 a clock the
 // same 2,048 clocks per 256 x 128 tile that the products take).  Two groups of 128 rows work in turns:
 // while one group's softmax runs, the tensor core works for the other.  Measured, 2,048 tokens of 64 heads of
-// 128 dims behind 14,336: 1,248-1,284 us, 803-826 TFLOP/s (half of the bf16 peak), 5,000 clocks a tile; the tensor
+// 128 dims behind 14,336: 1,248-1,288 us, 800-826 TFLOP/s (half of the bf16 peak), 5,000 clocks a tile; the tensor
 // pipe is active 40 % of the time, the exponential unit 34 %, issue slots 42 %: no unit is full, the softmax
 // warps' latencies and the half tiles' products (96 KB of shared memory reads each) add up.
 //
